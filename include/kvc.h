@@ -457,6 +457,100 @@ kvc_status kvc_block_compact(const kvc_layout* src_layout, const kvc_cache* src,
                              const kvc_layout* dst_layout, const kvc_cache* dst,
                              const int32_t* kept, int32_t keep, void* stream);
 
+/* ---- Serving operators on the dense cache -------------------------------
+ * KVC_DENSE_BF16 layouts (any head count, head_dim 64 or 128, out_bf16 0 or 1,
+ * softmax_scale, seq_lens and cache.layer as in kvc_decode_attn; KVC_EUNSUPPORTED
+ * for the other kinds): what a serving program runs beside the compressed
+ * decode -- prefill and decode with a bounded window, decode that records which
+ * tokens are used, eviction of the others, and a batch behind one shared prefix.
+ * No counterpart on the pages, except that eviction applies BellowsKV-Evict's
+ * keep decision ("Three Measurements, Three Operators") per KV head.
+ * Common to the four calls:
+ *   - Products of bf16 queries, keys and values accumulate in fp32, softmax
+ *     statistics are fp32.  With fp32 output the probabilities enter the value
+ *     product with 24 bits, with bf16 output with 16 (kvc_window_attn and
+ *     kvc_prefix_decode may use 8, the output's own width).
+ *   - Tokens that no query of a row sees (beyond its length, before its window)
+ *     may hold anything, NaN and infinities included: they never reach the
+ *     output.  A NaN or infinity that a query sees makes that query's output
+ *     non-finite, and no other's.
+ *   - A query that sees no token has a zero output.
+ *   - Results do not depend on the order in which blocks run.
+ *   - workspace, ws_bytes, the error word in its bytes 0..3 (zeroed by the call
+ *     before any kernel that can set it) and the checks before anything is
+ *     enqueued are those of kvc_decode_attn. */
+
+/* Device workspace bytes kvc_window_attn needs for contexts up to n_tokens and
+ * n_q query tokens per row.  0 for NULL or a layout the call does not take. */
+size_t kvc_window_workspace_bytes(const kvc_layout* layout, int32_t n_tokens, int32_t n_q);
+
+/* Attention of the last n_q tokens of every row over the row's cache, causal,
+ * with a sliding window and sinks: query i of row b stands at position
+ * p = len_b - n_q + i (its own key and value are already in the cache) and sees
+ * the tokens t <= p with t < sinks or t > p - window.  One token (decode), a
+ * chunk of a prefill or a whole prompt; window >= len_b is full causal
+ * attention.  Queries at negative positions (n_q > len_b) see nothing.
+ *   q: device bf16 [B, Hq, n_q, d], out: fp32 or bf16 of the same shape (all
+ *     layers at once, cache.layer = 0 with n_layers > 1: [n_layers, B, Hq, n_q, d]).
+ *   1 <= n_q <= max_tokens, window >= 1, sinks >= 0. */
+kvc_status kvc_window_attn(const kvc_layout* layout, const kvc_cache* cache, const void* q, int32_t n_q,
+                           int32_t window, int32_t sinks, void* out, void* workspace, size_t ws_bytes,
+                           void* stream);
+
+/* Device workspace bytes kvc_decode_accum needs (the scores of one step are
+ * part of them: 4 bytes per layer, query head and token). */
+size_t kvc_accum_workspace_bytes(const kvc_layout* layout, int32_t n_tokens);
+
+/* kvc_decode_attn on a dense layout that also adds to every token's running sum
+ * the attention weight it received:
+ *   weights[b][h][t] += sum over the query heads g of KV head h of
+ *                       softmax_t(scale * q[b][g] . k[b][h][t]),  t < len_b.
+ *   weights: device fp32 [B, Hkv, max_tokens] (all layers at once: [n_layers, B,
+ *     Hkv, max_tokens]), zeroed by the caller before the first step; entries at
+ *     t >= len_b are neither read nor written.
+ *   q, out: [B, Hq, d] as in kvc_decode_attn.  At most 4096 query heads per KV head. */
+kvc_status kvc_decode_accum(const kvc_layout* layout, const kvc_cache* cache, const void* q, float* weights,
+                            void* out, void* workspace, size_t ws_bytes, void* stream);
+
+/* Keep `keep` tokens of every row and KV head: the first `sinks`, the last
+ * `recent`, and of the others those with the largest running sums (ties: lower
+ * position first; NaN and negative sums count as zero), in their original order.
+ * Rows with at most keep tokens keep all.  Kept token i of a KV head becomes
+ * token i of dst, its sum dst_weights[..][i]; dst_weights[..][i] = 0 for new_len
+ * <= i < max_tokens of dst, so that tokens appended there start at zero.  Keys and
+ * values of dst beyond the new length are left as they were.  Different KV heads
+ * keep different tokens; keys keep the rotation they were stored with.
+ *   src, dst: caches of dense layouts with equal batch, KV heads, head_dim and
+ *     layers (cache.layer selects one layer, as elsewhere); keep <= max_tokens of
+ *     dst.  dst may be src itself, with equal max_tokens (in place; dst_weights may
+ *     then be weights).  No other overlap of what is written (KVC_EINVAL).
+ *   weights, dst_weights: device fp32 [B, Hkv, max_tokens of src / of dst].
+ *   kept: device int32 [B, Hkv, keep] (written), source positions in ascending
+ *     order, -1 beyond the new length.
+ *   new_lens: device int32 [B] (written): min(len_b, keep), the pos of the next
+ *     kvc_append and, once src->seq_lens is no longer needed, its successor.
+ *   (All layers at once: a leading n_layers axis on weights, dst_weights and kept.)
+ * keep >= 1, sinks, recent >= 0, sinks + recent <= keep. */
+kvc_status kvc_evict(const kvc_layout* src_layout, const kvc_cache* src, const kvc_layout* dst_layout,
+                     const kvc_cache* dst, const float* weights, float* dst_weights, int32_t keep,
+                     int32_t sinks, int32_t recent, int32_t* kept, int32_t* new_lens, void* stream);
+
+/* Device workspace bytes kvc_prefix_decode needs for contexts up to n_tokens
+ * own tokens behind n_prefix shared ones. */
+size_t kvc_prefix_workspace_bytes(const kvc_layout* layout, int32_t n_tokens, int32_t n_prefix);
+
+/* Single-token decode of a batch whose rows share one prefix: row b attends to
+ * the prefix's tokens and then to its own len_b tokens,
+ *   out[b][g] = softmax over both of (scale * q[b][g] . k) times v.
+ * The prefix is a dense cache of batch 1 (filled once by kvc_append); it is read
+ * once for the whole batch.  Both layouts have equal heads, head_dim, layers and
+ * softmax_scale.  Either part may be empty; with both empty the output is zero.
+ *   prefix->n_tokens (and prefix->seq_lens, [1]) give the prefix's length.
+ *   q, out: [B, Hq, d] as in kvc_decode_attn; out's type is layout's. */
+kvc_status kvc_prefix_decode(const kvc_layout* prefix_layout, const kvc_cache* prefix,
+                             const kvc_layout* layout, const kvc_cache* cache, const void* q, void* out,
+                             void* workspace, size_t ws_bytes, void* stream);
+
 /* ---- Joint rank / residual-bit allocation (host only) -------------------
  * "JoLT: Near-Lossless KV Cache Compression", section "How JoLT works": the
  * layers are grouped, the keys and the values of each group are separate

@@ -1,0 +1,100 @@
+// Internal declarations of the serving operators on the dense bf16 cache:
+// window attention, decode with accumulated weights, shared-prefix decode and
+// eviction.
+#pragma once
+
+#include "kvc_internal.h"
+
+namespace kvc {
+
+// One attention problem over a dense cache: `units` (row, KV head) pairs with
+// `rows` query rows each.  Row r of unit u stands at
+//   q + (u / Hkv) * q_row + (u % Hkv) * q_head + (r / r_div) * q_hi + (r % r_div) * d
+// (elements; the output has the same arrangement) and has position
+// len - n_q + r % n_q; it sees the tokens t <= position with t < sinks or
+// t > position - window.  The keys and values of unit u are rows
+// u * tmax .. u * tmax + len - 1 of k and v.
+struct DenseAttn {
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const __nv_bfloat16* q;
+  void* out;
+  int out_bf16;
+  int d, Hkv, units, rows;
+  long long q_row, q_head, q_hi;
+  int r_div;
+  int n_q, window, sinks;
+  int tmax, n_tokens;
+  const int* seq_lens;          // or null: every row holds n_tokens
+  int len_rows;                 // seq_lens entries (row u / Hkv reads entry % len_rows)
+  float scale_log2;             // softmax scale * log2(e)
+  float* scores;                // accumulated weights: scores [units, n_tokens, rows] in log2 units
+  // split partials: ((u * blocks + block) * splits + split) * row_block + row of the block,
+  // d accumulators each, and (maximum in log2 units, sum) pairs
+  int splits, row_block, blocks;
+  float* part;
+  float* ml;
+  int direct;                   // one split and nothing to merge with: the kernel writes the output
+  uint32_t* err;                // error word (bounded waits)
+};
+
+// Tokens that row unit u holds.
+__device__ __forceinline__ int dense_len(const DenseAttn& p, int u) {
+  int n = p.n_tokens;
+  if (p.seq_lens) {
+    const int s = p.seq_lens[(u / p.Hkv) % p.len_rows];
+    n = s < 0 ? 0 : (s < n ? s : n);
+  }
+  return n;
+}
+
+__host__ __device__ inline long long dense_row_at(const DenseAttn& p, int u, int r) {
+  return (long long)(u / p.Hkv) * p.q_row + (long long)(u % p.Hkv) * p.q_head +
+         (long long)(r / p.r_div) * p.q_hi + (long long)(r % p.r_div) * p.d;
+}
+
+// The tokens that a run of query positions [p_lo, p_hi] can see: [0, a1) and
+// [b0, b1); where they meet, one range [0, b1) with a1 = b0 = 0.
+struct TokenSpan {
+  int a1, b0, b1;
+};
+
+__host__ __device__ inline TokenSpan token_span(int p_lo, int p_hi, int window, int sinks) {
+  TokenSpan s = {0, 0, 0};
+  if (p_hi < 0) return s;
+  if (p_lo < 0) p_lo = 0;
+  s.b1 = p_hi + 1;
+  s.b0 = p_lo >= window ? p_lo - window + 1 : 0;
+  s.a1 = sinks < s.b1 ? sinks : s.b1;
+  if (s.a1 >= s.b0) s.a1 = s.b0 = 0;
+  return s;
+}
+
+// warp-level kernel (mma.sync): any number of rows, in blocks of up to 32
+int dense_row_block(int rows);
+int dense_splits(int units, int rows, long long tokens);
+cudaError_t launch_dense_attn(const DenseAttn& p, cudaStream_t s, bool overlap);
+
+// merge of one or two sets of split partials into the output
+cudaError_t launch_dense_combine(const DenseAttn& p, const DenseAttn* prefix, cudaStream_t s);
+
+// merge, and weights[u][t] += sum over the unit's rows of the attention weights
+cudaError_t launch_dense_accum(const DenseAttn& p, float* weights, cudaStream_t s);
+
+struct EvictCall {
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* k2;
+  __nv_bfloat16* v2;
+  const float* w;
+  float* w2;
+  int d, B, Hkv, units, tmax, tmax2, n_tokens;
+  const int* seq_lens;
+  int keep, sinks, recent;
+  int in_place;
+  int* kept;                    // [units, keep]
+  int* new_lens;                // [B]
+};
+cudaError_t launch_evict(const EvictCall& c, cudaStream_t s);
+
+}  // namespace kvc

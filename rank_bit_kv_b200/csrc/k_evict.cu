@@ -1,0 +1,247 @@
+// Eviction from a dense cache by accumulated attention weight, per KV head.
+//
+// Of the len tokens of a unit (row, KV head), the first `sinks` and the last
+// `recent` are kept always; the rest of the `keep` places go to the largest
+// running sums, equal ones to the lower position.  Kept tokens stay in order.
+//
+//   select_kernel  one block per unit.  A radix select over the sums' 32-bit
+//                  patterns (monotone for sums >= 0) finds the smallest kept sum
+//                  and how many tokens equal to it are kept; then each warp
+//                  counts its stretch of positions, the counts are scanned, and
+//                  each warp writes its kept positions.  Reads the sums once.
+//   gather kernels copy the kept rows of K and V and the sums: bound by memory,
+//                  4 d bytes read and written per kept token.
+#include <math.h>
+
+#include "dense_attn.h"
+#include "kvc_device.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;              // 11 bits a pass: 11 + 11 + 10
+constexpr int kStageTok = 48 * 1024;     // sums held in shared memory
+
+__device__ __forceinline__ int evict_len(const EvictCall& p, int u) {
+  int n = p.n_tokens;
+  if (p.seq_lens) {
+    const int s = p.seq_lens[(u / p.Hkv) % p.B];
+    n = s < 0 ? 0 : (s < n ? s : n);
+  }
+  return n;
+}
+
+__device__ __forceinline__ uint32_t sum_key(float w) { return w > 0.f ? __float_as_uint(w) : 0u; }
+
+template <bool STAGED>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictCall p) {
+  extern __shared__ uint32_t keys_sm[];  // STAGED: the candidates' keys
+  __shared__ unsigned hist[kBins];
+  __shared__ unsigned warp_a[kSelWarps], warp_b[kSelWarps];
+  __shared__ unsigned sh_digit, sh_need;
+  const int u = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int len = evict_len(p, u);
+  const int new_len = min(len, p.keep);
+  int* const kept = p.kept + (size_t)u * p.keep;
+  if (u < p.B * p.Hkv && u % p.Hkv == 0 && tid == 0) p.new_lens[u / p.Hkv] = new_len;
+  for (int i = new_len + tid; i < p.keep; i += kSelThreads) kept[i] = -1;
+  if (len <= p.keep) {
+    for (int i = tid; i < len; i += kSelThreads) kept[i] = i;
+    return;
+  }
+  // candidates: tokens [c0, c1), of which `need` are kept (sinks + recent <= keep < len)
+  const int c0 = p.sinks, c1 = len - p.recent;
+  const int n_c = c1 - c0;
+  unsigned need = (unsigned)(p.keep - p.sinks - p.recent);
+  const float* w = p.w + (size_t)u * p.tmax + c0;
+  auto key_at = [&](int i) { return STAGED ? keys_sm[i] : sum_key(w[i]); };
+  if (STAGED) {
+    for (int i = tid; i < n_c; i += kSelThreads) keys_sm[i] = sum_key(w[i]);
+  }
+  // the key of the need-th largest candidate, digit by digit from the top;
+  // need becomes the number of candidates equal to it that are kept
+  uint32_t prefix = 0;
+  int shift = 32;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int bits = pass == 2 ? 10 : 11;
+    const uint32_t hi = pass == 0 ? 0u : ~0u << shift;
+    shift -= bits;
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < n_c; i += kSelThreads) {
+      const uint32_t k = key_at(i);
+      if ((k & hi) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+    }
+    __syncthreads();
+    // suffix sums of the bins: thread t owns bins 2t, 2t + 1
+    const unsigned a = hist[2 * tid], b = hist[2 * tid + 1];
+    unsigned v = a + b;                  // sum over this lane and the lanes above it
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned x = __shfl_down_sync(0xffffffffu, v, o);
+      if (lane + o < 32) v += x;
+    }
+    if (lane == 0) warp_a[warp] = v;
+    __syncthreads();
+    unsigned above = 0;
+    for (int x = warp + 1; x < kSelWarps; ++x) above += warp_a[x];
+    const unsigned over = above + v - (a + b);        // candidates in bins above 2 tid + 1
+    if (need > over && need <= over + b) sh_digit = 2 * tid + 1, sh_need = need - over;
+    else if (need > over + b && need <= over + b + a) sh_digit = 2 * tid, sh_need = need - over - b;
+    if (need == 0 && tid == 0) sh_digit = kBins - 1, sh_need = 0;
+    __syncthreads();
+    prefix |= (sh_digit & ((1u << bits) - 1u)) << shift;
+    need = sh_need;
+  }
+  // need == 0 (nothing but the protected tokens): the key is above every sum
+  if (p.keep == p.sinks + p.recent) prefix = 0xffffffffu;
+  // each warp takes a stretch of positions [s0, s1) of the whole row
+  const int per = (len + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
+  const int s0 = min(len, warp * per), s1 = min(len, s0 + per);
+  // 2: kept, 1: equal to the boundary key, 0: not kept
+  auto cls = [&](int t) -> int {
+    if (t >= s1) return 0;
+    if (t < c0 || t >= c1) return 2;
+    const uint32_t k = key_at(t - c0);
+    return k > prefix ? 2 : k == prefix ? 1 : 0;
+  };
+  unsigned n_gt = 0, n_eq = 0;
+  for (int t = s0 + lane; t - lane < s1; t += 32) {
+    const int c = cls(t);
+    n_gt += __popc(__ballot_sync(0xffffffffu, c == 2));
+    n_eq += __popc(__ballot_sync(0xffffffffu, c == 1));
+  }
+  __syncthreads();
+  if (lane == 0) warp_a[warp] = n_gt, warp_b[warp] = n_eq;
+  __syncthreads();
+  unsigned at = 0, eq = 0;               // kept and equal tokens before this warp's stretch
+  for (int x = 0; x < warp; ++x) at += warp_a[x], eq += warp_b[x];
+  at += min(eq, need);
+  for (int t = s0 + lane; t - lane < s1; t += 32) {
+    const int c = cls(t);
+    const unsigned m1 = __ballot_sync(0xffffffffu, c == 1);
+    const unsigned before = __popc(m1 & ((1u << lane) - 1u));
+    const bool k = c == 2 || (c == 1 && eq + before < need);
+    const unsigned mk = __ballot_sync(0xffffffffu, k);
+    if (k) kept[at + __popc(mk & ((1u << lane) - 1u))] = t;
+    at += __popc(mk);
+    eq += __popc(m1);
+  }
+}
+
+// Kept rows into another cache: 16 bytes per thread, d / 8 threads per row.
+constexpr int kGThreads = 256;
+constexpr int kGUnroll = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kGThreads) gather_kernel(const __grid_constant__ EvictCall p) {
+  constexpr int TPR = D / 8, RPB = kGThreads / TPR;
+  const int nb = (p.keep + RPB * kGUnroll - 1) / (RPB * kGUnroll);      // blocks per unit and tensor
+  const int u = blockIdx.x / (2 * nb), b = blockIdx.x % (2 * nb), col = threadIdx.x % TPR;
+  const uint4* src = reinterpret_cast<const uint4*>(b >= nb ? p.v : p.k) + (size_t)u * p.tmax * TPR + col;
+  uint4* dst = reinterpret_cast<uint4*>(b >= nb ? p.v2 : p.k2) + (size_t)u * p.tmax2 * TPR + col;
+  const int i0 = b % nb * RPB * kGUnroll + threadIdx.x / TPR;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int* kept = p.kept + (size_t)u * p.keep;
+  int t[kGUnroll];
+  uint4 x[kGUnroll];
+#pragma unroll
+  for (int k = 0; k < kGUnroll; ++k) t[k] = i0 + k * RPB < p.keep ? kept[i0 + k * RPB] : -1;
+#pragma unroll
+  for (int k = 0; k < kGUnroll; ++k)
+    if (t[k] >= 0) x[k] = src[(size_t)t[k] * TPR];
+#pragma unroll
+  for (int k = 0; k < kGUnroll; ++k)
+    if (t[k] >= 0) dst[(size_t)(i0 + k * RPB) * TPR] = x[k];
+}
+
+// Kept rows moved down within one cache.  A block owns a 64-byte column of a
+// unit's rows (so that blocks do not meet) and takes the kept tokens in
+// order, a chunk at a time: kept[i] >= i, so a chunk's stores reach no row that
+// a later chunk still reads, and its own reads end before its stores begin.
+constexpr int kMoveTPR = 4, kMoveRows = kGThreads / kMoveTPR;
+
+template <int D>
+__global__ void __launch_bounds__(kGThreads) move_kernel(const __grid_constant__ EvictCall p) {
+  constexpr int TPR = D / 8, COLS = TPR / kMoveTPR;
+  const int u = blockIdx.x / (2 * COLS), part = blockIdx.x % (2 * COLS);
+  const int col = (part % COLS) * kMoveTPR + threadIdx.x % kMoveTPR;
+  uint4* rows = reinterpret_cast<uint4*>(part >= COLS ? p.v2 : p.k2) + (size_t)u * p.tmax2 * TPR + col;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int* kept = p.kept + (size_t)u * p.keep;
+  for (int i0 = threadIdx.x / kMoveTPR; i0 - (int)(threadIdx.x / kMoveTPR) < p.keep; i0 += kMoveRows * kGUnroll) {
+    int t[kGUnroll];
+    uint4 x[kGUnroll];
+#pragma unroll
+    for (int k = 0; k < kGUnroll; ++k) t[k] = i0 + k * kMoveRows < p.keep ? kept[i0 + k * kMoveRows] : -1;
+#pragma unroll
+    for (int k = 0; k < kGUnroll; ++k)
+      if (t[k] >= 0) x[k] = rows[(size_t)t[k] * TPR];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kGUnroll; ++k)
+      if (t[k] >= 0) rows[(size_t)(i0 + k * kMoveRows) * TPR] = x[k];
+  }
+}
+
+// The kept sums, in order and chunk by chunk as above (source and destination
+// may be one array); zero from the new length on.
+__global__ void __launch_bounds__(kSelThreads) gather_sums_kernel(const __grid_constant__ EvictCall p) {
+  const int u = blockIdx.x;
+  const float* src = p.w + (size_t)u * p.tmax;
+  float* dst = p.w2 + (size_t)u * p.tmax2;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int* kept = p.kept + (size_t)u * p.keep;
+  for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < p.tmax2; i0 += kSelThreads * 4) {
+    float x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * kSelThreads;
+      const int t = i < p.keep ? kept[i] : -1;
+      x[k] = t >= 0 ? src[t] : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i0 + k * kSelThreads < p.tmax2) dst[i0 + k * kSelThreads] = x[k];
+  }
+}
+
+template <int D>
+cudaError_t launch_rows(const EvictCall& c, cudaLaunchConfig_t& cfg) {
+  if (c.in_place) {
+    cfg.gridDim = dim3((unsigned)c.units * (2 * (D / 8) / kMoveTPR));
+    return cudaLaunchKernelEx(&cfg, move_kernel<D>, c);
+  }
+  const int per = kGThreads / (D / 8) * kGUnroll;
+  cfg.gridDim = dim3((unsigned)c.units * 2 * ((c.keep + per - 1) / per));
+  return cudaLaunchKernelEx(&cfg, gather_kernel<D>, c);
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictCall& c, cudaStream_t s) {
+  cudaError_t e;
+  const int n_c = c.n_tokens - c.sinks - c.recent;      // candidates of the longest row
+  if (n_c <= kStageTok) {
+    const int bytes = n_c > 0 ? n_c * 4 : 0;
+    e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageTok * 4);
+    if (e != cudaSuccess) return e;
+    select_kernel<true><<<c.units, kSelThreads, bytes, s>>>(c);
+  } else {
+    select_kernel<false><<<c.units, kSelThreads, 0, s>>>(c);
+  }
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cfg.blockDim = dim3(kGThreads);
+  e = c.d == 128 ? launch_rows<128>(c, cfg) : launch_rows<64>(c, cfg);
+  if (e != cudaSuccess) return e;
+  gather_sums_kernel<<<c.units, kSelThreads, 0, s>>>(c);
+  return cudaGetLastError();
+}
+
+}  // namespace kvc

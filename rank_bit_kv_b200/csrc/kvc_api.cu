@@ -10,17 +10,6 @@
 
 #include "kvc_internal.h"
 
-struct kvc_layout {
-  kvc_layout_desc d;
-  int G, L, ngk, ngv;
-  int lk_row, lv_row, lksz_row, lvsz_row;  // bytes per row
-  int64_t rows;                             // rows per low-rank component
-  int qdim, vdim;
-  int units;                                // independent (row, head) units of the split kernel
-  size_t sizes[KVC_NBUF];
-  float scale;
-};
-
 namespace {
 
 thread_local std::string g_err;

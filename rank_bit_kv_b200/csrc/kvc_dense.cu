@@ -1,0 +1,296 @@
+// Entry points of the serving operators on dense bf16 layouts: argument
+// checks, workspace sizes and the choice of kernel.
+#include <string.h>
+
+#include "dense_attn.h"
+
+namespace {
+
+using kvc::report_error;
+
+constexpr size_t kHeader = 256;          // workspace: error word
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+kvc_status ok() { return report_error(KVC_OK, "%s", ""); }
+
+kvc_status launched(cudaError_t e, const char* what) {
+  return e == cudaSuccess ? ok() : report_error(KVC_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// Layers that a call on this cache covers.
+int layers(const kvc_layout* L, const kvc_cache* c) { return c->layer > 0 ? 1 : L->L; }
+
+// The cache of a dense layout as an attention problem of n_q query tokens per row.
+kvc_status dense_problem(const char* what, const kvc_layout* L, const kvc_cache* c, int n_q,
+                         kvc::DenseAttn* p) {
+  const kvc_layout_desc& d = L->d;
+  memset(p, 0, sizeof(*p));
+  if (d.kind != KVC_DENSE_BF16) return report_error(KVC_EUNSUPPORTED, "%s: dense bf16 layouts only", what);
+  if (c->n_tokens < 0) return report_error(KVC_EINVAL, "%s: n_tokens %d < 0", what, c->n_tokens);
+  if (c->n_tokens > d.max_tokens)
+    return report_error(KVC_ECAPACITY, "%s: n_tokens %d > max_tokens %d", what, c->n_tokens, d.max_tokens);
+  if (c->layer < 0 || c->layer > L->L)
+    return report_error(KVC_EINVAL, "%s: cache.layer %d outside 0..%d", what, c->layer, L->L);
+  if (!c->k_dense || !c->v_dense) return report_error(KVC_EINVAL, "%s: cache.k_dense / v_dense is NULL", what);
+  if (!aligned16(c->k_dense) || !aligned16(c->v_dense) || !aligned16(c->seq_lens))
+    return report_error(KVC_EALIGN, "%s: cache buffers must be 16-byte aligned", what);
+  const size_t layer_elems = (size_t)d.batch * d.n_kv_heads * d.max_tokens * d.head_dim;
+  const size_t skip = c->layer > 0 ? (size_t)(c->layer - 1) * layer_elems : 0;
+  p->k = (const __nv_bfloat16*)c->k_dense + skip;
+  p->v = (const __nv_bfloat16*)c->v_dense + skip;
+  p->out_bf16 = d.out_bf16;
+  p->d = d.head_dim;
+  p->Hkv = d.n_kv_heads;
+  p->units = layers(L, c) * d.batch * d.n_kv_heads;
+  p->n_q = n_q;
+  p->rows = L->G * n_q;
+  p->r_div = p->rows;
+  p->q_head = (long long)p->rows * d.head_dim;
+  p->q_row = p->q_head * d.n_kv_heads;
+  p->window = d.max_tokens;              // every position
+  p->sinks = 0;
+  p->tmax = d.max_tokens;
+  p->n_tokens = c->n_tokens;
+  p->seq_lens = c->seq_lens;
+  p->len_rows = d.batch;
+  p->scale_log2 = L->scale * 1.4426950408889634f;
+  return KVC_OK;
+}
+
+kvc_status check_io(const char* what, const void* q, const void* out) {
+  if (!q || !out) return report_error(KVC_EINVAL, "%s: q / out is NULL", what);
+  if (!aligned16(q) || !aligned16(out)) return report_error(KVC_EALIGN, "%s: q / out must be 16-byte aligned", what);
+  return KVC_OK;
+}
+
+kvc_status check_ws(const char* what, const void* ws, size_t size, size_t need) {
+  if (!ws || size < need) return report_error(KVC_EWORKSPACE, "%s: workspace %zu bytes < %zu needed", what, size, need);
+  if (!aligned16(ws)) return report_error(KVC_EALIGN, "%s: workspace must be 16-byte aligned", what);
+  return KVC_OK;
+}
+
+// Grids are one-dimensional and the row indexes of a unit are ints.
+bool too_large(long long units, long long rows) {
+  return rows > (1ll << 30) || units * ((rows + 7) / 8) > (1ll << 30) || units * rows > (1ll << 31) - 1;
+}
+
+// Partials of a problem (in row blocks), and their bytes.  dense_splits()
+// stops once its blocks pass four waves of the SMs, so it never asks for more
+// than eight (a last doubling of the blocks may follow).
+size_t part_blocks(long long units, long long rows, long long tokens) {
+  const int rb = kvc::dense_row_block((int)rows);
+  const size_t blocks = (size_t)(units * ((rows + rb - 1) / rb));
+  const size_t most = blocks * (size_t)((tokens + 127) / 128 > 1 ? (tokens + 127) / 128 : 1);
+  const size_t cap = blocks + 4 * kvc::kNumSMs;
+  return most < cap ? most : cap;
+}
+
+size_t part_bytes(long long units, long long rows, long long tokens, int d) {
+  const size_t n = part_blocks(units, rows, tokens) * kvc::dense_row_block((int)rows);
+  return round_up(n * d * 4, 256) + round_up(n * 8, 256);
+}
+
+// Fill in the split plan over `tokens` tokens and place the partials at `at`.
+void place_parts(kvc::DenseAttn* p, long long tokens, char* at) {
+  p->row_block = kvc::dense_row_block(p->rows);
+  p->blocks = (p->rows + p->row_block - 1) / p->row_block;
+  p->splits = kvc::dense_splits(p->units, p->rows, tokens);
+  const size_t n = (size_t)p->units * p->blocks * p->splits * p->row_block;
+  p->part = (float*)at;
+  p->ml = (float*)(at + round_up(n * p->d * 4, 256));
+}
+
+}  // namespace
+
+extern "C" size_t kvc_window_workspace_bytes(const kvc_layout* L, int32_t n_tokens, int32_t n_q) {
+  if (!L || L->d.kind != KVC_DENSE_BF16 || n_q < 1) return 0;
+  const long long units = (long long)L->L * L->d.batch * L->d.n_kv_heads, rows = (long long)L->G * n_q;
+  if (too_large(units, rows)) return 0;
+  size_t most = part_bytes(units, rows, n_tokens, L->d.head_dim);
+  if (L->L > 1) {                        // one layer alone splits further
+    const size_t one = part_bytes(units / L->L, rows, n_tokens, L->d.head_dim);
+    if (one > most) most = one;
+  }
+  return kHeader + most;
+}
+
+extern "C" kvc_status kvc_window_attn(const kvc_layout* L, const kvc_cache* c, const void* q, int32_t n_q,
+                                      int32_t window, int32_t sinks, void* out, void* workspace,
+                                      size_t ws_size, void* stream) {
+  const char* what = "kvc_window_attn";
+  if (!L || !c) return report_error(KVC_EINVAL, "%s: NULL argument", what);
+  if (n_q < 1 || window < 1 || sinks < 0)
+    return report_error(KVC_EINVAL, "%s: n_q %d (>= 1), window %d (>= 1), sinks %d (>= 0)", what, n_q, window, sinks);
+  if (n_q > L->d.max_tokens)
+    return report_error(KVC_ECAPACITY, "%s: n_q %d > max_tokens %d", what, n_q, L->d.max_tokens);
+  if (too_large((long long)L->L * L->d.batch * L->d.n_kv_heads, (long long)L->G * n_q))
+    return report_error(KVC_EUNSUPPORTED, "%s: more than 2^31 - 1 query rows", what);
+  kvc::DenseAttn p;
+  kvc_status st = dense_problem(what, L, c, n_q, &p);
+  if (st != KVC_OK || (st = check_io(what, q, out)) != KVC_OK) return st;
+  if ((st = check_ws(what, workspace, ws_size, kvc_window_workspace_bytes(L, c->n_tokens, n_q))) != KVC_OK) return st;
+  p.q = (const __nv_bfloat16*)q;
+  p.out = out;
+  if (window < p.window) p.window = window;
+  p.sinks = sinks < p.tmax ? sinks : p.tmax;
+  p.err = (uint32_t*)workspace;
+  // tokens that a block of rows reads
+  long long span = (long long)p.window + p.sinks + (n_q > 32 ? 32 : n_q);
+  if (span > c->n_tokens) span = c->n_tokens;
+  place_parts(&p, span, (char*)workspace + kHeader);
+  p.direct = p.splits == 1;
+  cudaGetLastError();
+  cudaStream_t s = (cudaStream_t)stream;
+  st = launched(kvc::launch_dense_attn(p, s, false), "window attention launch");
+  if (st != KVC_OK || p.direct) return st;
+  return launched(kvc::launch_dense_combine(p, nullptr, s), "window attention merge launch");
+}
+
+extern "C" size_t kvc_accum_workspace_bytes(const kvc_layout* L, int32_t n_tokens) {
+  const size_t w = kvc_window_workspace_bytes(L, n_tokens, 1);
+  if (w == 0) return 0;
+  return w + round_up((size_t)L->L * L->d.batch * L->d.n_q_heads * (size_t)(n_tokens > 0 ? n_tokens : 0) * 4, 256);
+}
+
+extern "C" kvc_status kvc_decode_accum(const kvc_layout* L, const kvc_cache* c, const void* q, float* weights,
+                                       void* out, void* workspace, size_t ws_size, void* stream) {
+  const char* what = "kvc_decode_accum";
+  if (!L || !c || !weights) return report_error(KVC_EINVAL, "%s: NULL argument", what);
+  if (L->G > 4096) return report_error(KVC_EUNSUPPORTED, "%s: %d query heads per KV head (at most 4096)", what, L->G);
+  kvc::DenseAttn p;
+  kvc_status st = dense_problem(what, L, c, 1, &p);
+  if (st != KVC_OK || (st = check_io(what, q, out)) != KVC_OK) return st;
+  if (!aligned16(weights)) return report_error(KVC_EALIGN, "%s: weights must be 16-byte aligned", what);
+  if ((st = check_ws(what, workspace, ws_size, kvc_accum_workspace_bytes(L, c->n_tokens))) != KVC_OK) return st;
+  p.q = (const __nv_bfloat16*)q;
+  p.out = out;
+  p.err = (uint32_t*)workspace;
+  char* at = (char*)workspace + kHeader;
+  p.scores = (float*)at;
+  at += round_up((size_t)p.units * p.rows * (size_t)c->n_tokens * 4, 256);
+  place_parts(&p, c->n_tokens, at);
+  cudaGetLastError();
+  cudaStream_t s = (cudaStream_t)stream;
+  st = launched(kvc::launch_dense_attn(p, s, false), "weighted decode launch");
+  if (st != KVC_OK) return st;
+  return launched(kvc::launch_dense_accum(p, weights, s), "weight sum launch");
+}
+
+extern "C" size_t kvc_prefix_workspace_bytes(const kvc_layout* L, int32_t n_tokens, int32_t n_prefix) {
+  const size_t w = kvc_window_workspace_bytes(L, n_tokens, 1);
+  if (w == 0) return 0;
+  const long long units = (long long)L->L * L->d.n_kv_heads, rows = (long long)L->d.batch * L->G;
+  size_t most = part_bytes(units, rows, n_prefix, L->d.head_dim);
+  if (L->L > 1) {
+    const size_t one = part_bytes(units / L->L, rows, n_prefix, L->d.head_dim);
+    if (one > most) most = one;
+  }
+  return w + most;
+}
+
+extern "C" kvc_status kvc_prefix_decode(const kvc_layout* PL, const kvc_cache* pc, const kvc_layout* L,
+                                        const kvc_cache* c, const void* q, void* out, void* workspace,
+                                        size_t ws_size, void* stream) {
+  const char* what = "kvc_prefix_decode";
+  if (!PL || !pc || !L || !c) return report_error(KVC_EINVAL, "%s: NULL argument", what);
+  kvc::DenseAttn p, pre;
+  kvc_status st = dense_problem(what, L, c, 1, &p);
+  if (st != KVC_OK || (st = dense_problem(what, PL, pc, 1, &pre)) != KVC_OK) return st;
+  if (PL->d.batch != 1) return report_error(KVC_EINVAL, "%s: the prefix layout has batch %d (1)", what, PL->d.batch);
+  if (PL->d.n_kv_heads != L->d.n_kv_heads || PL->d.n_q_heads != L->d.n_q_heads || PL->d.head_dim != L->d.head_dim ||
+      layers(PL, pc) != layers(L, c))
+    return report_error(KVC_EINVAL, "%s: the two layouts differ in heads, head_dim or layers", what);
+  if (PL->scale != L->scale) return report_error(KVC_EINVAL, "%s: the two layouts differ in softmax_scale", what);
+  if ((st = check_io(what, q, out)) != KVC_OK) return st;
+  if ((st = check_ws(what, workspace, ws_size, kvc_prefix_workspace_bytes(L, c->n_tokens, pc->n_tokens))) != KVC_OK)
+    return st;
+  p.q = pre.q = (const __nv_bfloat16*)q;
+  p.out = pre.out = out;
+  p.err = pre.err = (uint32_t*)workspace;
+  // the prefix's rows: every query head of the KV head's group, of every batch row
+  pre.out_bf16 = p.out_bf16;
+  pre.rows = L->d.batch * L->G;
+  pre.r_div = L->G;
+  pre.q_hi = p.q_row;
+  pre.q_row = p.q_row * L->d.batch;
+  pre.q_head = p.q_head;
+  char* at = (char*)workspace + kHeader;
+  place_parts(&p, c->n_tokens, at);
+  at += part_bytes(p.units, p.rows, c->n_tokens, p.d);
+  place_parts(&pre, pc->n_tokens, at);
+  cudaGetLastError();
+  cudaStream_t s = (cudaStream_t)stream;
+  st = launched(kvc::launch_dense_attn(pre, s, false), "prefix attention launch");
+  if (st != KVC_OK) return st;
+  st = launched(kvc::launch_dense_attn(p, s, false), "own tokens' attention launch");
+  if (st != KVC_OK) return st;
+  return launched(kvc::launch_dense_combine(p, &pre, s), "prefix merge launch");
+}
+
+extern "C" kvc_status kvc_evict(const kvc_layout* SL, const kvc_cache* src, const kvc_layout* DL,
+                                const kvc_cache* dst, const float* weights, float* dst_weights,
+                                int32_t keep, int32_t sinks, int32_t recent, int32_t* kept,
+                                int32_t* new_lens, void* stream) {
+  const char* what = "kvc_evict";
+  if (!SL || !src || !DL || !dst || !weights || !dst_weights || !kept || !new_lens)
+    return report_error(KVC_EINVAL, "%s: NULL argument", what);
+  kvc::DenseAttn a, b;
+  kvc_status st = dense_problem(what, SL, src, 1, &a);
+  if (st != KVC_OK || (st = dense_problem(what, DL, dst, 1, &b)) != KVC_OK) return st;
+  if (SL->d.batch != DL->d.batch || a.Hkv != b.Hkv || a.d != b.d || a.units != b.units)
+    return report_error(KVC_EINVAL, "%s: the two layouts differ in batch, KV heads, head_dim or layers", what);
+  if (keep < 1 || sinks < 0 || recent < 0 || (long long)sinks + recent > keep)
+    return report_error(KVC_EINVAL, "%s: keep %d (>= 1), sinks %d and recent %d (>= 0, together at most keep)", what,
+                        keep, sinks, recent);
+  if (keep > b.tmax)
+    return report_error(KVC_ECAPACITY, "%s: keep %d > the destination's max_tokens %d", what, keep, b.tmax);
+  if (!aligned16(weights) || !aligned16(dst_weights) || !aligned16(kept) || !aligned16(new_lens))
+    return report_error(KVC_EALIGN, "%s: pointers must be 16-byte aligned", what);
+  if ((long long)a.units * ((keep + 63) / 64) > (1ll << 27))
+    return report_error(KVC_EUNSUPPORTED, "%s: too many kept rows for one call", what);
+  // each destination is its own source (in place) or shares no byte with any
+  // array that the call reads or writes
+  const size_t rows1 = (size_t)a.units * a.tmax, rows2 = (size_t)b.units * b.tmax;
+  struct Span { const char* p; size_t n; };
+  auto span = [](const void* p, size_t n) { return Span{(const char*)p, n}; };
+  const Span in[4] = {span(a.k, rows1 * a.d * 2), span(a.v, rows1 * a.d * 2), span(weights, rows1 * 4),
+                      span(src->seq_lens, src->seq_lens ? (size_t)SL->d.batch * 4 : 0)};
+  const Span to[5] = {span(b.k, rows2 * b.d * 2), span(b.v, rows2 * b.d * 2), span(dst_weights, rows2 * 4),
+                      span(kept, (size_t)a.units * keep * 4), span(new_lens, (size_t)SL->d.batch * 4)};
+  const bool in_place = b.k == a.k && b.v == a.v && a.tmax == b.tmax;
+  auto meet = [](const Span& x, const Span& y) { return x.n && y.n && x.p < y.p + y.n && y.p < x.p + x.n; };
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 4; ++j) {
+      const bool same = i == j && ((i < 2 && in_place) || (i == 2 && to[2].p == in[2].p && a.tmax == b.tmax));
+      if (!same && meet(to[i], in[j]))
+        return report_error(KVC_EINVAL, "%s: a destination overlaps a source (in place: the same cache and sums)", what);
+    }
+    for (int j = 0; j < i; ++j)
+      if (meet(to[i], to[j])) return report_error(KVC_EINVAL, "%s: two destinations overlap", what);
+  }
+  kvc::EvictCall e;
+  e.k = a.k;
+  e.v = a.v;
+  e.k2 = const_cast<__nv_bfloat16*>(b.k);
+  e.v2 = const_cast<__nv_bfloat16*>(b.v);
+  e.w = weights;
+  e.w2 = dst_weights;
+  e.d = a.d;
+  e.B = SL->d.batch;
+  e.Hkv = a.Hkv;
+  e.units = a.units;
+  e.tmax = a.tmax;
+  e.tmax2 = b.tmax;
+  e.n_tokens = src->n_tokens;
+  e.seq_lens = src->seq_lens;
+  e.keep = keep;
+  e.sinks = sinks;
+  e.recent = recent;
+  e.in_place = in_place;
+  e.kept = kept;
+  e.new_lens = new_lens;
+  cudaGetLastError();
+  return launched(kvc::launch_evict(e, (cudaStream_t)stream), "evict launch");
+}

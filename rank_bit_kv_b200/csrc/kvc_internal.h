@@ -8,6 +8,18 @@
 
 #include "../../include/kvc.h"
 
+// A validated layout with its closed-form sizes (the handle of the C ABI).
+struct kvc_layout {
+  kvc_layout_desc d;
+  int G, L, ngk, ngv;
+  int lk_row, lv_row, lksz_row, lvsz_row;  // bytes per row
+  int64_t rows;                             // rows per low-rank component
+  int qdim, vdim;
+  int units;                                // independent (row, head) units of the split kernel
+  size_t sizes[KVC_NBUF];
+  float scale;
+};
+
 namespace kvc {
 
 constexpr int kMaxBatch = 256;

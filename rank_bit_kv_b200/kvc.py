@@ -114,6 +114,21 @@ def lib():
         L.kvc_block_compact.argtypes = [vp, C.POINTER(CacheDesc), vp, C.POINTER(CacheDesc), vp,
                                         i32, vp]
         L.kvc_block_compact.restype = C.c_int
+        cdp = C.POINTER(CacheDesc)
+        L.kvc_window_workspace_bytes.argtypes = [vp, i32, i32]
+        L.kvc_window_workspace_bytes.restype = sz
+        L.kvc_window_attn.argtypes = [vp, cdp, vp, i32, i32, i32, vp, vp, sz, vp]
+        L.kvc_window_attn.restype = C.c_int
+        L.kvc_accum_workspace_bytes.argtypes = [vp, i32]
+        L.kvc_accum_workspace_bytes.restype = sz
+        L.kvc_decode_accum.argtypes = [vp, cdp, vp, vp, vp, vp, sz, vp]
+        L.kvc_decode_accum.restype = C.c_int
+        L.kvc_evict.argtypes = [vp, cdp, vp, cdp, vp, vp, i32, i32, i32, vp, vp, vp]
+        L.kvc_evict.restype = C.c_int
+        L.kvc_prefix_workspace_bytes.argtypes = [vp, i32, i32]
+        L.kvc_prefix_workspace_bytes.restype = sz
+        L.kvc_prefix_decode.argtypes = [vp, cdp, vp, cdp, vp, vp, vp, sz, vp]
+        L.kvc_prefix_decode.restype = C.c_int
         L.kvc_select_rope_kernel.argtypes = [i32]
         L.kvc_select_rope_kernel.restype = None
         L.kvc_select_varrate_kernel.argtypes = [i32]
@@ -190,6 +205,12 @@ class Layout:
         check(lib().kvc_buffer_sizes(self.h, arr))
         return dict(zip(BUFS, list(arr)))
 
+    def buffer_sizes_cached(self):
+        """buffer_sizes(), asked once (a layout is immutable)."""
+        if getattr(self, "_sizes", None) is None:
+            self._sizes = self.buffer_sizes()
+        return self._sizes
+
     def workspace_bytes(self, n_tokens):
         return int(lib().kvc_workspace_bytes(self.h, n_tokens))
 
@@ -198,6 +219,15 @@ class Layout:
 
     def decode_launches(self, n_tokens):
         return int(lib().kvc_decode_launches(self.h, n_tokens))
+
+    def window_workspace_bytes(self, n_tokens, n_q=1):
+        return int(lib().kvc_window_workspace_bytes(self.h, n_tokens, n_q))
+
+    def accum_workspace_bytes(self, n_tokens):
+        return int(lib().kvc_accum_workspace_bytes(self.h, n_tokens))
+
+    def prefix_workspace_bytes(self, n_tokens, n_prefix):
+        return int(lib().kvc_prefix_workspace_bytes(self.h, n_tokens, n_prefix))
 
 
 def _ptr(t):
@@ -474,3 +504,140 @@ def block_compact(src_layout, src_cache, dst_layout, dst_cache, kept, stream=Non
     check(lib().kvc_block_compact(src_layout.h, C.byref(a), dst_layout.h, C.byref(b), _ptr(kept),
                                   int(kept.shape[1]), st))
     dst_cache.n_tokens = int(kept.shape[1])
+
+
+# --------------------------------------------------------------------------- serving operators
+#
+# On dense bf16 layouts.  Tensors are contiguous and on one device; a call whose
+# tensors are not on the current device makes theirs current for its duration.
+# `stream` is a cudaStream_t (default: torch's current stream of that device).
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(t, name, dtype, shape, device):
+    """t's address, after the checks that the C ABI cannot make."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _on(device, stream, call):
+    """call(stream) with `device` current; raises what the library reports."""
+    import torch
+
+    _need(device.type == "cuda", f"the tensors are on {device}, not on a GPU")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _on(device, stream, call)
+    check(call(torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream))
+
+
+def _dense_dims(layout, cache):
+    """(leading layer axis, batch, query heads, KV heads, head dim) of a dense call."""
+    d = layout.desc
+    _need(d.kind == KVC_DENSE_BF16, "the serving operators take dense layouts")
+    lead = (d.n_layers,) if d.n_layers > 1 and not cache.layer else ()
+    return lead, d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim
+
+
+def _check_cache(cache, device, batch):
+    import torch
+
+    sizes = cache.layout.buffer_sizes_cached()
+    for name in ("k_dense", "v_dense"):
+        t = cache.bufs[name]
+        _need(t.device == device and t.numel() * t.element_size() >= sizes[name] and t.is_contiguous(),
+              f"cache.{name} must be a contiguous buffer of {sizes[name]} bytes on {device}")
+    if cache.seq_lens is not None:
+        _tensor(cache.seq_lens, "cache.seq_lens", torch.int32, (batch,), device)
+
+
+def _check_ws(ws, device):
+    _need(ws.device == device and ws.is_contiguous(), f"ws must be a contiguous buffer on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def window_attn(layout: Layout, cache: Cache, q, out, ws, window, sinks=0, stream=None):
+    """kvc_window_attn: causal attention of the last n_q tokens of every row, each
+    seeing the last `window` tokens up to itself and the first `sinks`.
+    q bf16 [B, Hq, n_q, d]; out fp32 or bf16 (the layout's) of the same shape;
+    ws at least layout.window_workspace_bytes(cache.n_tokens, n_q) bytes."""
+    import torch
+
+    lead, B, Hq, _, d = _dense_dims(layout, cache)
+    dev = q.device
+    _need(q.dim() == 4 + len(lead), "q must be [B, Hq, n_q, d] (all layers at once: [n_layers, B, Hq, n_q, d])")
+    n_q = q.shape[-2]
+    shape = (*lead, B, Hq, n_q, d)
+    qp = _tensor(q, "q", torch.bfloat16, shape, dev)
+    op = _tensor(out, "out", torch.bfloat16 if layout.desc.out_bf16 else torch.float32, shape, dev)
+    _check_cache(cache, dev, B)
+    wp, wn = _check_ws(ws, dev)
+    cs = cache.struct()
+    _on(dev, stream, lambda st: lib().kvc_window_attn(layout.h, cs, qp, n_q, window, sinks, op, wp, wn, st))
+
+
+def decode_accum(layout: Layout, cache: Cache, q, weights, out, ws, stream=None):
+    """kvc_decode_accum: single-token decode that adds every token's attention
+    weight to weights fp32 [B, Hkv, max_tokens].  q bf16 [B, Hq, d]; out fp32 or
+    bf16 of that shape; ws at least layout.accum_workspace_bytes(cache.n_tokens)."""
+    import torch
+
+    lead, B, Hq, Hkv, d = _dense_dims(layout, cache)
+    dev, shape = q.device, (*lead, B, Hq, d)
+    qp = _tensor(q, "q", torch.bfloat16, shape, dev)
+    op = _tensor(out, "out", torch.bfloat16 if layout.desc.out_bf16 else torch.float32, shape, dev)
+    ap = _tensor(weights, "weights", torch.float32, (*lead, B, Hkv, layout.desc.max_tokens), dev)
+    _check_cache(cache, dev, B)
+    wp, wn = _check_ws(ws, dev)
+    cs = cache.struct()
+    _on(dev, stream, lambda st: lib().kvc_decode_accum(layout.h, cs, qp, ap, op, wp, wn, st))
+
+
+def evict(src_layout: Layout, src_cache: Cache, dst_layout: Layout, dst_cache: Cache, weights, dst_weights,
+          keep, sinks=0, recent=0, stream=None):
+    """kvc_evict: keep the `keep` tokens of every row and KV head with the largest
+    running sums (the first `sinks` and last `recent` always), compacted into
+    dst_cache (which may be src_cache) and dst_weights.  Returns (kept int32
+    [B, Hkv, keep], new_lens int32 [B]).  The caller sets the destination's
+    n_tokens and seq_lens (new_lens) afterwards."""
+    import torch
+
+    lead, B, _, Hkv, _ = _dense_dims(src_layout, src_cache)
+    lead2, B2, _, Hkv2, _ = _dense_dims(dst_layout, dst_cache)
+    dev = weights.device
+    ap = _tensor(weights, "weights", torch.float32, (*lead, B, Hkv, src_layout.desc.max_tokens), dev)
+    bp = _tensor(dst_weights, "dst_weights", torch.float32, (*lead2, B2, Hkv2, dst_layout.desc.max_tokens), dev)
+    _check_cache(src_cache, dev, B)
+    _check_cache(dst_cache, dev, B2)
+    kept = torch.empty((*lead, B, Hkv, max(0, int(keep))), dtype=torch.int32, device=dev)
+    lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    a, b = src_cache.struct(), dst_cache.struct()
+    _on(dev, stream, lambda st: lib().kvc_evict(src_layout.h, a, dst_layout.h, b, ap, bp, keep, sinks, recent,
+                                                kept.data_ptr() or None, lens.data_ptr(), st))
+    return kept, lens
+
+
+def prefix_decode(prefix_layout: Layout, prefix_cache: Cache, layout: Layout, cache: Cache, q, out, ws,
+                  stream=None):
+    """kvc_prefix_decode: single-token decode of rows that share the tokens of
+    prefix_cache (a dense cache of batch 1) and continue with their own in cache.
+    q bf16 [B, Hq, d]; out fp32 or bf16 of that shape; ws at least
+    layout.prefix_workspace_bytes(cache.n_tokens, prefix_cache.n_tokens) bytes."""
+    import torch
+
+    lead, B, Hq, _, d = _dense_dims(layout, cache)
+    _dense_dims(prefix_layout, prefix_cache)
+    dev, shape = q.device, (*lead, B, Hq, d)
+    qp = _tensor(q, "q", torch.bfloat16, shape, dev)
+    op = _tensor(out, "out", torch.bfloat16 if layout.desc.out_bf16 else torch.float32, shape, dev)
+    _check_cache(prefix_cache, dev, 1)
+    _check_cache(cache, dev, B)
+    wp, wn = _check_ws(ws, dev)
+    a, b = prefix_cache.struct(), cache.struct()
+    _on(dev, stream, lambda st: lib().kvc_prefix_decode(prefix_layout.h, a, layout.h, b, qp, op, wp, wn, st))
