@@ -9,10 +9,11 @@ namespace kvc {
 
 // One attention problem over a dense cache: `units` (row, KV head) pairs with
 // `rows` query rows each.  Row r of unit u stands at
-//   q + (u / Hkv) * q_row + (u % Hkv) * q_head + (r / r_div) * q_hi + (r % r_div) * d
-// (elements; the output has the same arrangement) and has position
-// len - n_q + r % n_q; it sees the tokens t <= position with t < sinks or
-// t > position - window.  The keys and values of unit u are rows
+//   q + (u / Hkv) * q_row + (u % Hkv) * q_head + (r / r_div) * q_hi + (r % r_div) * q_lo
+// (elements; the output has the same arrangement).  With several query tokens
+// (n_q > 1) r_div is the number of query heads, so that the rows of a block are
+// close in position: len - n_q + r / r_div; with one it is len - 1.  A row sees the
+// tokens t <= position with t < sinks or t > position - window.  The keys and values of unit u are rows
 // u * tmax .. u * tmax + len - 1 of k and v.
 struct DenseAttn {
   const __nv_bfloat16* k;
@@ -21,7 +22,7 @@ struct DenseAttn {
   void* out;
   int out_bf16;
   int d, Hkv, units, rows;
-  long long q_row, q_head, q_hi;
+  long long q_row, q_head, q_hi, q_lo;
   int r_div;
   int n_q, window, sinks;
   int tmax, n_tokens;
@@ -36,6 +37,8 @@ struct DenseAttn {
   float* ml;
   int direct;                   // one split and nothing to merge with: the kernel writes the output
   uint32_t* err;                // error word (bounded waits)
+  int clear_err;                // the kernel clears it first
+  int tensor;                   // the tcgen05 kernel
 };
 
 // Tokens that row unit u holds.
@@ -50,7 +53,11 @@ __device__ __forceinline__ int dense_len(const DenseAttn& p, int u) {
 
 __host__ __device__ inline long long dense_row_at(const DenseAttn& p, int u, int r) {
   return (long long)(u / p.Hkv) * p.q_row + (long long)(u % p.Hkv) * p.q_head +
-         (long long)(r / p.r_div) * p.q_hi + (long long)(r % p.r_div) * p.d;
+         (long long)(r / p.r_div) * p.q_hi + (long long)(r % p.r_div) * p.q_lo;
+}
+
+__host__ __device__ inline int dense_row_pos(const DenseAttn& p, int len, int r) {
+  return p.n_q == 1 ? len - 1 : len - p.n_q + r / p.r_div;
 }
 
 // The tokens that a run of query positions [p_lo, p_hi] can see: [0, a1) and
@@ -70,10 +77,16 @@ __host__ __device__ inline TokenSpan token_span(int p_lo, int p_hi, int window, 
   return s;
 }
 
-// warp-level kernel (mma.sync): any number of rows, in blocks of up to 32
-int dense_row_block(int rows);
-int dense_splits(int units, int rows, long long tokens);
-cudaError_t launch_dense_attn(const DenseAttn& p, cudaStream_t s, bool overlap);
+constexpr int kTensorRows = 64;          // rows from which the tcgen05 kernel is taken
+constexpr int kWaves = 4;
+
+struct DensePlan {
+  int tensor, row_block, blocks, splits;
+};
+DensePlan dense_plan(int units, int rows, long long tokens, int out_bf16);
+long long dense_part_rows(long long units, long long rows, long long tokens, int out_bf16, bool direct);
+cudaError_t launch_dense_attn(const DenseAttn& p, cudaStream_t s);
+cudaError_t launch_dense_attn_tc(const DenseAttn& p, cudaStream_t s);
 
 // merge of one or two sets of split partials into the output
 cudaError_t launch_dense_combine(const DenseAttn& p, const DenseAttn* prefix, cudaStream_t s);

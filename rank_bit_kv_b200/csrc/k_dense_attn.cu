@@ -14,8 +14,7 @@
 // writes one partial per row, or the output where nothing is left to merge.
 #include <math.h>
 
-#include "dense_attn.h"
-#include "kvc_device.cuh"
+#include "dense_rows.cuh"
 #include "tc_util.cuh"
 
 namespace kvc {
@@ -64,59 +63,6 @@ __device__ __forceinline__ bool sees(int t, int pos, int window, int sinks) {
   return t <= pos && (t < sinks || t > pos - window);
 }
 
-// One output row from its definition, by one warp, reading only the tokens the
-// row sees.  Taken for a row of a several-token call whose result is not
-// finite: a NaN or infinite value of a token that the row does not see, but
-// another row of its tile does, enters the tile product as 0 * NaN.
-template <int D>
-__device__ void row_alone(const DenseAttn& p, int u, int r, float (&o)[D / 32]) {
-  const int lane = threadIdx.x & 31;
-  const int pos = dense_len(p, u) - p.n_q + r % p.n_q;
-  const __nv_bfloat16* qr = p.q + dense_row_at(p, u, r);
-  float qv[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    qv[i] = bf2f(qr[lane + 32 * i]) * p.scale_log2;
-    o[i] = 0.f;
-  }
-  const TokenSpan sp = token_span(pos, pos, p.window, p.sinks);
-  float m = -INFINITY, l = 0.f;
-  for (int t = sp.a1 ? 0 : sp.b0; t < sp.b1; t = (t + 1 == sp.a1) ? sp.b0 : t + 1) {
-    const size_t row = ((size_t)u * p.tmax + t) * D;
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) x = fmaf(qv[i], bf2f(p.k[row + lane + 32 * i]), x);
-    x = warp_sum(x);
-    const float nm = fmaxf(m, x);
-    const float a = m == -INFINITY ? 0.f : exp2f(m - nm);
-    const float w = x == -INFINITY ? 0.f : exp2f(x - nm);
-    l = l * a + w;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = o[i] * a + w * bf2f(p.v[row + lane + 32 * i]);
-    m = nm;
-  }
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) o[i] = l == 0.f ? 0.f : o[i] / l;
-}
-
-// Write a finished row (value i of lane `lane` is dim lane + 32 i).
-template <int D>
-__device__ __forceinline__ void put_row(const DenseAttn& p, int u, int r, float (&o)[D / 32]) {
-  const int lane = threadIdx.x & 31;
-  if (p.n_q > 1) {
-    bool fine = true;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) fine = fine && fabsf(o[i]) <= 3.4e38f;
-    if (!__all_sync(0xffffffffu, fine)) row_alone<D>(p, u, r, o);
-  }
-  const long long at = dense_row_at(p, u, r);
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[at + lane + 32 * i] = __float2bfloat16_rn(o[i]);
-    else reinterpret_cast<float*>(p.out)[at + lane + 32 * i] = o[i];
-  }
-}
-
 // NT: 8-row tiles of a row block.  EXACT (fp32 output): the probabilities
 // enter the value product in three bf16 parts (24 bits), and each tile's product
 // is formed from zero and added in fp32 arithmetic -- the MMA's own accumulation
@@ -137,12 +83,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(const __grid_co
   const int n_rows = min(RB, p.rows - r0);
   const int len = dense_len(p, u);
 
-  // positions of this block's rows (those of one query head run upwards)
-  int p_lo = len - p.n_q, p_hi = len - 1;
-  if (MODE == kManyTokens) {
-    const int i0 = r0 % p.n_q, i1 = i0 + n_rows - 1;
-    if (i1 < p.n_q) p_lo = len - p.n_q + i0, p_hi = len - p.n_q + i1;
-  }
+  // positions of this block's rows (ascending)
+  int p_lo = len - 1, p_hi = len - 1;
+  if (MODE == kManyTokens) p_lo = dense_row_pos(p, len, r0), p_hi = dense_row_pos(p, len, r0 + n_rows - 1);
   const TokenSpan sp = token_span(p_lo, p_hi, p.window, p.sinks);
   const int n_a = (sp.a1 + kTok - 1) / kTok;
   const int n_tiles = n_a + (sp.b1 - sp.b0 + kTok - 1) / kTok;
@@ -198,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(const __grid_co
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) pos[nt][e] = len - p.n_q + (r0 + 8 * nt + 2 * c4 + e) % p.n_q;
+      for (int e = 0; e < 2; ++e) pos[nt][e] = dense_row_pos(p, len, min(r0 + 8 * nt + 2 * c4 + e, p.rows - 1));
   }
   float m_ref[NT][2], l_sum[NT][2], acc[KS][NT][4];
 #pragma unroll
@@ -390,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(const __grid_co
     if (p.direct) {
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) o[i] = l == 0.f ? 0.f : o[i] / l;
-      put_row<D>(p, u, r0 + r, o);
+      dense_put_row<D>(p, u, r0 + r, o);
     } else {
       const size_t at = (size_t)blockIdx.x * RB + r;
 #pragma unroll
@@ -470,7 +413,7 @@ __device__ void merge_row(const DenseAttn& p, int u, int r, const PartRef* set, 
       for (int w = 0; w < kCWarps; ++w) t += red[w][lane + 32 * i];
       o[i] = l == 0.f ? 0.f : t / l;
     }
-    put_row<D>(p, u, r, o);
+    dense_put_row<D>(p, u, r, o);
   }
 }
 
@@ -561,14 +504,36 @@ cudaError_t launch_d(const DenseAttn& p, cudaLaunchConfig_t& cfg) {
 
 }  // namespace
 
-int dense_row_block(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
-
-// Splits of a unit's tokens: enough blocks for every SM (one block runs per
-// SM), none with fewer tiles than warps; where the units alone exceed the SMs,
-// as few splits as fill whole waves of blocks to nine tenths.
-int dense_splits(int units, int rows, long long tokens) {
-  const int rb = dense_row_block(rows);
-  const long long blocks = (long long)units * ((rows + rb - 1) / rb);
+// The kernel and the split of a problem's tokens.
+//
+// Warp-level kernel: blocks of up to 32 rows, one block per SM at a time; enough
+// splits for every SM, none with fewer tiles than warps; where the blocks alone
+// exceed the SMs, as few splits as fill whole waves to nine tenths.
+//
+// tcgen05 kernel: bf16 output and at least kTensorRows rows per KV head.  256 rows
+// per block where rows and tokens give every SM a block, 128 otherwise; splits of
+// at least two tiles per score stream up to one block per SM.
+DensePlan dense_plan(int units, int rows, long long tokens, int out_bf16) {
+  DensePlan f;
+  if (out_bf16 && rows >= kTensorRows) {
+    const long long tiles = (tokens + 127) / 128, wide = (long long)units * ((rows + 255) / 256);
+    f.tensor = 1;
+    f.row_block = rows > 128 && wide * (tiles / 2 > 1 ? tiles / 2 : 1) >= kNumSMs ? 256 : 128;
+    f.blocks = (rows + f.row_block - 1) / f.row_block;
+    const long long ctas = (long long)units * f.blocks, most = tiles / (f.row_block == 256 ? 2 : 4);
+    long long s = kNumSMs / ctas;
+    s = s < most ? s : most;
+    if (s > 1) {
+      const long long per = (tiles + s - 1) / s;
+      s = (tiles + per - 1) / per;
+    }
+    f.splits = s > 1 ? (int)s : 1;
+    return f;
+  }
+  f.tensor = 0;
+  f.row_block = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  f.blocks = (rows + f.row_block - 1) / f.row_block;
+  const long long blocks = (long long)units * f.blocks;
   const long long most = (tokens + kTok * kWarps - 1) / (kTok * kWarps);
   long long best = 1;
   double best_fill = 0.;
@@ -576,17 +541,37 @@ int dense_splits(int units, int rows, long long tokens) {
     const long long waves = (blocks * s + kNumSMs - 1) / kNumSMs;
     const double fill = (double)(blocks * s) / (double)(waves * kNumSMs);
     if (fill > best_fill + 0.02) best = s, best_fill = fill;
-    if (fill >= 0.9 || blocks * s > 4 * kNumSMs) break;
+    if (fill >= 0.9 || blocks * s > kWaves * kNumSMs) break;
   }
-  return (int)best;
+  f.splits = (int)best;
+  return f;
 }
 
-cudaError_t launch_dense_attn(const DenseAttn& p, cudaStream_t s, bool overlap) {
+// Row slots that the partials take in any call of up to `tokens` tokens and, with
+// `direct`, of up to `rows` rows (a call of one split then writes its output and
+// needs none).
+long long dense_part_rows(long long units, long long rows, long long tokens, int out_bf16, bool direct) {
+  const long long tiles = tokens > 128 ? (tokens + 127) / 128 : 1;
+  if (out_bf16 && rows >= kTensorRows) {
+    // splits only while the blocks do not fill the SMs
+    const long long wide = units * ((rows + 255) / 256);
+    if (wide >= kNumSMs && !direct) return wide * 256;
+    return 256 * (wide * tiles < kNumSMs ? wide * tiles : kNumSMs);
+  }
+  // splits until the blocks pass kWaves waves, and none where they do without
+  const int rb = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  const long long nb = units * ((rows + rb - 1) / rb);
+  if (nb > kWaves * kNumSMs && !direct) return nb * rb;
+  const long long most = (nb < kWaves * kNumSMs ? nb : kWaves * kNumSMs) + kWaves * kNumSMs;
+  return rb * (nb * tiles < most ? nb * tiles : most);
+}
+
+cudaError_t launch_dense_attn(const DenseAttn& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)p.units * p.blocks * p.splits));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
-  (void)overlap;
+  if (p.tensor) return launch_dense_attn_tc(p, s);
   return p.d == 128 ? launch_d<128>(p, cfg) : launch_d<64>(p, cfg);
 }
 

@@ -46,7 +46,9 @@ kvc_status dense_problem(const char* what, const kvc_layout* L, const kvc_cache*
   p->units = layers(L, c) * d.batch * d.n_kv_heads;
   p->n_q = n_q;
   p->rows = L->G * n_q;
-  p->r_div = p->rows;
+  p->r_div = L->G;
+  p->q_hi = d.head_dim;
+  p->q_lo = (long long)n_q * d.head_dim;
   p->q_head = (long long)p->rows * d.head_dim;
   p->q_row = p->q_head * d.n_kv_heads;
   p->window = d.max_tokens;              // every position
@@ -76,27 +78,22 @@ bool too_large(long long units, long long rows) {
   return rows > (1ll << 30) || units * ((rows + 7) / 8) > (1ll << 30) || units * rows > (1ll << 31) - 1;
 }
 
-// Partials of a problem (in row blocks), and their bytes.  dense_splits()
-// stops once its blocks pass four waves of the SMs, so it never asks for more
-// than eight (a last doubling of the blocks may follow).
-size_t part_blocks(long long units, long long rows, long long tokens) {
-  const int rb = kvc::dense_row_block((int)rows);
-  const size_t blocks = (size_t)(units * ((rows + rb - 1) / rb));
-  const size_t most = blocks * (size_t)((tokens + 127) / 128 > 1 ? (tokens + 127) / 128 : 1);
-  const size_t cap = blocks + 4 * kvc::kNumSMs;
-  return most < cap ? most : cap;
-}
-
-size_t part_bytes(long long units, long long rows, long long tokens, int d) {
-  const size_t n = part_blocks(units, rows, tokens) * kvc::dense_row_block((int)rows);
-  return round_up(n * d * 4, 256) + round_up(n * 8, 256);
+// Bytes of the partials of a problem, for all layers of a layout or one of them
+// (one alone may split further).
+size_t part_bytes(const kvc_layout* L, long long units, long long rows, long long tokens, bool bf16, bool direct) {
+  long long n = kvc::dense_part_rows(units * L->L, rows, tokens, bf16, direct);
+  const long long one = kvc::dense_part_rows(units, rows, tokens, bf16, direct);
+  if (one > n) n = one;
+  return round_up((size_t)n * L->d.head_dim * 4, 256) + round_up((size_t)n * 8, 256);
 }
 
 // Fill in the split plan over `tokens` tokens and place the partials at `at`.
 void place_parts(kvc::DenseAttn* p, long long tokens, char* at) {
-  p->row_block = kvc::dense_row_block(p->rows);
-  p->blocks = (p->rows + p->row_block - 1) / p->row_block;
-  p->splits = kvc::dense_splits(p->units, p->rows, tokens);
+  const kvc::DensePlan f = kvc::dense_plan(p->units, p->rows, tokens, p->out_bf16 && !p->scores);
+  p->tensor = p->clear_err = f.tensor;
+  p->row_block = f.row_block;
+  p->blocks = f.blocks;
+  p->splits = f.splits;
   const size_t n = (size_t)p->units * p->blocks * p->splits * p->row_block;
   p->part = (float*)at;
   p->ml = (float*)(at + round_up(n * p->d * 4, 256));
@@ -106,14 +103,9 @@ void place_parts(kvc::DenseAttn* p, long long tokens, char* at) {
 
 extern "C" size_t kvc_window_workspace_bytes(const kvc_layout* L, int32_t n_tokens, int32_t n_q) {
   if (!L || L->d.kind != KVC_DENSE_BF16 || n_q < 1) return 0;
-  const long long units = (long long)L->L * L->d.batch * L->d.n_kv_heads, rows = (long long)L->G * n_q;
-  if (too_large(units, rows)) return 0;
-  size_t most = part_bytes(units, rows, n_tokens, L->d.head_dim);
-  if (L->L > 1) {                        // one layer alone splits further
-    const size_t one = part_bytes(units / L->L, rows, n_tokens, L->d.head_dim);
-    if (one > most) most = one;
-  }
-  return kHeader + most;
+  const long long units = (long long)L->d.batch * L->d.n_kv_heads, rows = (long long)L->G * n_q;
+  if (too_large(units * L->L, rows)) return 0;
+  return kHeader + part_bytes(L, units, rows, n_tokens, L->d.out_bf16, true);
 }
 
 extern "C" kvc_status kvc_window_attn(const kvc_layout* L, const kvc_cache* c, const void* q, int32_t n_q,
@@ -136,22 +128,24 @@ extern "C" kvc_status kvc_window_attn(const kvc_layout* L, const kvc_cache* c, c
   if (window < p.window) p.window = window;
   p.sinks = sinks < p.tmax ? sinks : p.tmax;
   p.err = (uint32_t*)workspace;
-  // tokens that a block of rows reads
-  long long span = (long long)p.window + p.sinks + (n_q > 32 ? 32 : n_q);
+  // tokens that a block of rows reads, for the split (a block is at most 256 rows)
+  const int at_once = L->G < 256 ? 256 / L->G : 1;
+  long long span = (long long)p.window + p.sinks + (n_q < at_once ? n_q : at_once) - 1;
   if (span > c->n_tokens) span = c->n_tokens;
   place_parts(&p, span, (char*)workspace + kHeader);
   p.direct = p.splits == 1;
   cudaGetLastError();
   cudaStream_t s = (cudaStream_t)stream;
-  st = launched(kvc::launch_dense_attn(p, s, false), "window attention launch");
+  st = launched(kvc::launch_dense_attn(p, s), "window attention launch");
   if (st != KVC_OK || p.direct) return st;
   return launched(kvc::launch_dense_combine(p, nullptr, s), "window attention merge launch");
 }
 
 extern "C" size_t kvc_accum_workspace_bytes(const kvc_layout* L, int32_t n_tokens) {
-  const size_t w = kvc_window_workspace_bytes(L, n_tokens, 1);
-  if (w == 0) return 0;
-  return w + round_up((size_t)L->L * L->d.batch * L->d.n_q_heads * (size_t)(n_tokens > 0 ? n_tokens : 0) * 4, 256);
+  if (!L || L->d.kind != KVC_DENSE_BF16) return 0;
+  const long long units = (long long)L->d.batch * L->d.n_kv_heads;
+  if (too_large(units * L->L, L->G)) return 0;
+  return kHeader + part_bytes(L, units, L->G, n_tokens, false, false) + round_up((size_t)L->L * L->d.batch * L->d.n_q_heads * (size_t)(n_tokens > 0 ? n_tokens : 0) * 4, 256);
 }
 
 extern "C" kvc_status kvc_decode_accum(const kvc_layout* L, const kvc_cache* c, const void* q, float* weights,
@@ -173,21 +167,17 @@ extern "C" kvc_status kvc_decode_accum(const kvc_layout* L, const kvc_cache* c, 
   place_parts(&p, c->n_tokens, at);
   cudaGetLastError();
   cudaStream_t s = (cudaStream_t)stream;
-  st = launched(kvc::launch_dense_attn(p, s, false), "weighted decode launch");
+  st = launched(kvc::launch_dense_attn(p, s), "weighted decode launch");
   if (st != KVC_OK) return st;
   return launched(kvc::launch_dense_accum(p, weights, s), "weight sum launch");
 }
 
 extern "C" size_t kvc_prefix_workspace_bytes(const kvc_layout* L, int32_t n_tokens, int32_t n_prefix) {
-  const size_t w = kvc_window_workspace_bytes(L, n_tokens, 1);
-  if (w == 0) return 0;
-  const long long units = (long long)L->L * L->d.n_kv_heads, rows = (long long)L->d.batch * L->G;
-  size_t most = part_bytes(units, rows, n_prefix, L->d.head_dim);
-  if (L->L > 1) {
-    const size_t one = part_bytes(units / L->L, rows, n_prefix, L->d.head_dim);
-    if (one > most) most = one;
-  }
-  return w + most;
+  if (!L || L->d.kind != KVC_DENSE_BF16) return 0;
+  const long long units = (long long)L->d.batch * L->d.n_kv_heads;
+  if (too_large(units * L->L, L->G) || too_large((long long)L->L * L->d.n_kv_heads, (long long)L->d.batch * L->G)) return 0;
+  return kHeader + part_bytes(L, units, L->G, n_tokens, L->d.out_bf16, false) +
+         part_bytes(L, L->d.n_kv_heads, (long long)L->d.batch * L->G, n_prefix, L->d.out_bf16, false);
 }
 
 extern "C" kvc_status kvc_prefix_decode(const kvc_layout* PL, const kvc_cache* pc, const kvc_layout* L,
@@ -218,13 +208,13 @@ extern "C" kvc_status kvc_prefix_decode(const kvc_layout* PL, const kvc_cache* p
   pre.q_head = p.q_head;
   char* at = (char*)workspace + kHeader;
   place_parts(&p, c->n_tokens, at);
-  at += part_bytes(p.units, p.rows, c->n_tokens, p.d);
+  at += part_bytes(L, (long long)L->d.batch * p.Hkv, p.rows, c->n_tokens, p.out_bf16, false);
   place_parts(&pre, pc->n_tokens, at);
   cudaGetLastError();
   cudaStream_t s = (cudaStream_t)stream;
-  st = launched(kvc::launch_dense_attn(pre, s, false), "prefix attention launch");
+  st = launched(kvc::launch_dense_attn(pre, s), "prefix attention launch");
   if (st != KVC_OK) return st;
-  st = launched(kvc::launch_dense_attn(p, s, false), "own tokens' attention launch");
+  st = launched(kvc::launch_dense_attn(p, s), "own tokens' attention launch");
   if (st != KVC_OK) return st;
   return launched(kvc::launch_dense_combine(p, &pre, s), "prefix merge launch");
 }
