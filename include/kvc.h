@@ -610,6 +610,13 @@ kvc_status kvc_allocate_rank_bits(int32_t n_cells, int32_t n_options, const doub
  * the pages. */
 void kvc_test_skip_tile_copies(int32_t on);
 
+/* Workspace bytes that a serving operator's plan uses (host only; op 0
+ * kvc_window_attn with n_2 query tokens, 1 kvc_decode_accum, 2 kvc_prefix_decode
+ * with n_2 prefix tokens; layer as in cache.layer), for the test that it stays
+ * within the size queries.  -1 for arguments the calls refuse. */
+int64_t kvc_test_dense_plan_bytes(const kvc_layout* layout, int32_t op, int32_t n_tokens, int32_t n_2,
+                                  int32_t window, int32_t sinks, int32_t layer);
+
 /* Kernel choice for pre-RoPE INT4 layouts (per calling thread): 0 (default)
  * and 1 run the warp-level kernel (reconstruction on mma.sync, fp32
  * accumulate; the faster of the two on the benchmark layout as measured), 2

@@ -13,8 +13,25 @@ namespace kvc {
 // (elements; the output has the same arrangement).  With several query tokens
 // (n_q > 1) r_div is the number of query heads, so that the rows of a block are
 // close in position: len - n_q + r / r_div; with one it is len - 1.  A row sees the
-// tokens t <= position with t < sinks or t > position - window.  The keys and values of unit u are rows
-// u * tmax .. u * tmax + len - 1 of k and v.
+// tokens t <= position with t < sinks or t > position - window.  The keys and values
+// of unit u are rows u * tmax .. u * tmax + len - 1 of k and v.
+//
+// Partials of a problem whose tokens are split: row r of unit u has split s at
+//   ((u * blocks + r / row_block) * splits + s) * row_block + r % row_block,
+// d accumulators and (maximum in log2 units, sum) each.  Flat: the tiles of all row
+// blocks v = u * blocks + r / row_block in a row are dealt out to kFlatGroups groups
+// of `splits` warps in equal stretches; the parts of v are slots (g0 + v) * splits ..
+// (g1 + v + 1) * splits - 1 of row_block rows, g0 .. g1 the groups that meet it.
+struct PartSet {
+  float* part;
+  float* ml;
+  int splits, row_block, blocks;
+  // the tiles' layout, for flat
+  int flat, Hkv, layers;
+  const int* lens;
+  int n_lens, n_tokens, n_q, window, sinks;
+};
+
 struct DenseAttn {
   const __nv_bfloat16* k;
   const __nv_bfloat16* v;
@@ -29,16 +46,17 @@ struct DenseAttn {
   const int* seq_lens;          // or null: every row holds n_tokens
   int len_rows;                 // seq_lens entries (row u / Hkv reads entry % len_rows)
   float scale_log2;             // softmax scale * log2(e)
-  float* scores;                // accumulated weights: scores [units, n_tokens, rows] in log2 units
-  // split partials: ((u * blocks + block) * splits + split) * row_block + row of the block,
-  // d accumulators each, and (maximum in log2 units, sum) pairs
-  int splits, row_block, blocks;
-  float* part;
-  float* ml;
-  int direct;                   // one split and nothing to merge with: the kernel writes the output
+  float* weights;               // accumulated weights [units, tmax], or null
+  float* scores;                // scores [units, n_tokens, rows] in log2 units, where they stay in global memory
+  int score_stride;             // else: floats per row of the scores in shared memory
+  PartSet own;                  // the split of this problem
+  int finish;                   // the kernel merges the splits and writes the output (no partials)
+  PartSet pre;                  // shared prefix: its partials (part null: none), whose unit is the KV head and
+  int pre_batch;                // whose rows run over the batch's rows too
   uint32_t* err;                // error word (bounded waits)
   int clear_err;                // the kernel clears it first
   int tensor;                   // the tcgen05 kernel
+  int wide;                     // blocks of eight warps, one per SM
 };
 
 // Tokens that row unit u holds.
@@ -79,20 +97,33 @@ __host__ __device__ inline TokenSpan token_span(int p_lo, int p_hi, int window, 
 
 constexpr int kTensorRows = 64;          // rows from which the tcgen05 kernel is taken
 constexpr int kWaves = 4;
+constexpr int kMaxCluster = 16;          // splits that one cluster merges
+
+constexpr int kFlatGroups = 128;         // blocks of the flat kernel (see there)
+constexpr int kFlatTiles = 8;            // tiles per warp in it, at least
+constexpr int kFlatFrom = 32768;         // 8 KB tiles from which a call goes flat and pays for a merge,
+constexpr int kFlatMerge = 6144;         // and where there is a second kernel anyway
 
 struct DensePlan {
-  int tensor, row_block, blocks, splits;
+  int tensor, flat, wide, row_block, blocks, splits;
+  long long slots;              // partials, of row_block rows each
 };
-DensePlan dense_plan(int units, int rows, long long tokens, int out_bf16);
-long long dense_part_rows(long long units, long long rows, long long tokens, int out_bf16, bool direct);
-cudaError_t launch_dense_attn(const DenseAttn& p, cudaStream_t s);
+DensePlan dense_plan(int units, int group, int n_q, int d, long long tokens, int out_bf16, int flat_from);
+// the split of decode with weights: scores in shared memory (score_stride > 0) where they fit
+DensePlan dense_accum_plan(int units, int rows, int d, long long tokens, int* score_stride);
+long long dense_part_rows(long long units, long long group, long long n_q, long long tokens, int out_bf16,
+                          bool direct);
+
+// dependent: may start before the preceding launch on the stream ends (it waits
+// for it before it reads p.pre)
+cudaError_t launch_dense_attn(const DenseAttn& p, cudaStream_t s, bool dependent);
 cudaError_t launch_dense_attn_tc(const DenseAttn& p, cudaStream_t s);
 
-// merge of one or two sets of split partials into the output
-cudaError_t launch_dense_combine(const DenseAttn& p, const DenseAttn* prefix, cudaStream_t s);
+// merge of the split partials (and the prefix's) into the output
+cudaError_t launch_dense_combine(const DenseAttn& p, cudaStream_t s);
 
 // merge, and weights[u][t] += sum over the unit's rows of the attention weights
-cudaError_t launch_dense_accum(const DenseAttn& p, float* weights, cudaStream_t s);
+cudaError_t launch_dense_accum(const DenseAttn& p, cudaStream_t s);
 
 struct EvictCall {
   const __nv_bfloat16* k;

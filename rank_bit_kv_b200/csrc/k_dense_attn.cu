@@ -10,8 +10,10 @@
 // values) through its own cp.async ring, with no block barrier in the loop;
 // the rows of a KV head (query heads x query tokens) are the N dimension of the
 // MMAs, so a tile is read once for all of them.  A block's warps take the
-// tiles of its token range in turn, merge in shared memory, and the block
-// writes one partial per row, or the output where nothing is left to merge.
+// tiles of its token range in turn and merge in shared memory.  Up to 16 splits of
+// a unit are one cluster: its blocks merge through distributed shared memory and
+// write the output in the same launch, and with accumulated weights the scores
+// never leave shared memory.  More splits write partials for a second kernel.
 #include <math.h>
 
 #include "dense_rows.cuh"
@@ -23,17 +25,24 @@ namespace {
 using namespace tc;
 
 constexpr int kTok = 16;                 // tokens per tile
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kSlots = 2 * kNumSMs;      // two blocks per SM
+constexpr int kMaxSmem = 216 * 1024;     // dynamic shared memory of a block, at most
 
 enum Mode { kOneToken = 0, kManyTokens = 1, kScores = 2 };
+enum Shape { kSmall = 0, kWide = 1 };
 
-template <int D>
+// Warps of a block and tiles in their rings.  Small calls: two blocks of four warps
+// per SM.  Large ones (kWide): one block of eight -- a tile's chain of scores,
+// exponentials and products is latency, which takes that many warps to hide (of
+// half tiles, 16) -- with one tile in flight behind the one in work: more of them
+// only crowd the memory (1.07 GB: 170 us with two tiles, 171 with three, 186 with
+// twelve warps of two).
+template <int D, int NT, int MODE, int SHAPE>
 struct Geo {
-  static constexpr int kRowB = 2 * D + 16;               // shared bytes per token row (no bank conflicts)
-  static constexpr int kTileB = kTok * kRowB;
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kWarpB = kStages * 2 * kTileB;
+  static constexpr int kWarps = SHAPE == kSmall ? 4 : D == 64 && NT == 1 ? 16 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStages = (SHAPE == kSmall && MODE != kScores ? 3 : 2) * (kWarps == 16 ? 1 : 128 / D);
+  static constexpr int kWarpB = kStages * 2 * kTok * (2 * D + 16);
   static constexpr int kSmem = kWarps * kWarpB;
 };
 
@@ -63,105 +72,247 @@ __device__ __forceinline__ bool sees(int t, int pos, int window, int sinks) {
   return t <= pos && (t < sinks || t > pos - window);
 }
 
-// NT: 8-row tiles of a row block.  EXACT (fp32 output): the probabilities
-// enter the value product in three bf16 parts (24 bits), and each tile's product
-// is formed from zero and added in fp32 arithmetic -- the MMA's own accumulation
-// truncates, which over a long context adds up to more than fp32's rounding.
-// Otherwise two parts (16 bits, well below the output's 8), accumulated by the MMA.
-template <int D, int NT, bool EXACT, int MODE>
-__global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(const __grid_constant__ DenseAttn p) {
-  using G = Geo<D>;
-  constexpr int RB = 8 * NT;
-  constexpr int KS = D / 16;             // k-steps of the scores, m-tiles of the values
-  constexpr int CPR = D / 8;             // 16-byte chunks per row
-  extern __shared__ __align__(128) uint8_t dsm[];
-  __shared__ float sm_ml[kWarps][RB][2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, c4 = lane & 3;
-  const int split = blockIdx.x % p.splits, ub = blockIdx.x / p.splits;
-  const int u = ub / p.blocks, r0 = (ub % p.blocks) * RB;
-  const int n_rows = min(RB, p.rows - r0);
-  const int len = dense_len(p, u);
+// A part that saw nothing holds zeros; NaN scores leave its maximum at -inf with
+// a NaN sum, which must reach the result.
+__device__ __forceinline__ bool empty_part(float m, float l) { return m == -INFINITY && l == 0.f; }
+__device__ __forceinline__ float part_scale(float m, float mx) { return m == -INFINITY ? 1.f : exp2f(m - mx); }
 
-  // positions of this block's rows (ascending)
-  int p_lo = len - 1, p_hi = len - 1;
-  if (MODE == kManyTokens) p_lo = dense_row_pos(p, len, r0), p_hi = dense_row_pos(p, len, r0 + n_rows - 1);
-  const TokenSpan sp = token_span(p_lo, p_hi, p.window, p.sinks);
-  const int n_a = (sp.a1 + kTok - 1) / kTok;
-  const int n_tiles = n_a + (sp.b1 - sp.b0 + kTok - 1) / kTok;
-  const int per = (n_tiles + p.splits - 1) / p.splits;
-  const int j_end = min(n_tiles, (split + 1) * per);
-  const int j_first = split * per + warp;          // this warp: every kWarps-th tile from here
-  const int n_mine = j_first < j_end ? (j_end - j_first + kWarps - 1) / kWarps : 0;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t map_rank(uint32_t smem, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem), "r"(rank));
+  return r;
+}
+template <int E>
+__device__ __forceinline__ void ld_cluster_row(uint32_t a, float (&x)[E]) {
+  if (E == 4)
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[E - 2]), "=f"(x[E - 1])
+                 : "r"(a));
+  else asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "r"(a));
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
 
-  uint8_t* ring = dsm + warp * G::kWarpB;
-  const uint8_t* const kb = reinterpret_cast<const uint8_t*>(p.k + (size_t)u * p.tmax * D);
-  const uint8_t* const vb = reinterpret_cast<const uint8_t*>(p.v + (size_t)u * p.tmax * D);
-  auto tile_at = [&](int i, int& t0, int& nt) {
-    const int j = j_first + i * kWarps;
-    t0 = j < n_a ? j * kTok : sp.b0 + (j - n_a) * kTok;
-    nt = min(kTok, (j < n_a ? sp.a1 : sp.b1) - t0);
-  };
-  // copy tile i of this warp into its ring stage (rows past the range are zero)
-  auto issue = [&](int i) {
-    int t0, nt;
-    tile_at(i, t0, nt);
-    const uint8_t* ks = kb + (size_t)t0 * (2 * D);
-    const uint8_t* vs = vb + (size_t)t0 * (2 * D);
-    uint8_t* st = ring + (i % G::kStages) * (2 * G::kTileB);
+// Where lane s holds part s of up to 32: the largest maximum, the merged sum, each
+// part's scale and which parts are empty.
+struct Scales {
+  float mx, l, a;
+  unsigned empty;
+};
+__device__ __forceinline__ Scales scales(float2 x, float mx) {
+  Scales f;
+  const bool none = empty_part(x.x, x.y);
+  f.mx = mx;
+  f.a = none ? 0.f : part_scale(x.x, mx);
+  f.l = warp_sum(none ? 0.f : f.a * x.y);
+  f.empty = __ballot_sync(0xffffffffu, none);
+  return f;
+}
+__device__ __forceinline__ float2 no_part() { return make_float2(-INFINITY, 0.f); }
+
+// A row's parts in the cluster's n blocks.
+__device__ __forceinline__ Scales cluster_scales(const float2* fin, int n) {
+  const int lane = threadIdx.x & 31;
+  const float2 x = lane < n ? ld_cluster_f2(map_rank(smem_u32(fin), lane)) : no_part();
+  return scales(x, warp_max(x.x));
+}
+
+// Row r's split partials in a set: first index, and how many.
+struct PartRef {
+  const float* part;
+  const float* ml;
+  size_t first;                          // partial of split 0; split s is s * step further
+  int step, n;
+};
+
+// Tiles of a unit of batch row b.
+__device__ __forceinline__ int unit_tiles(const PartSet& f, int b) {
+  int n = f.n_tokens;
+  if (f.lens) n = min(max(f.lens[b], 0), n);
+  const TokenSpan sp = token_span(n - f.n_q, n - 1, f.window, f.sinks);
+  return (sp.a1 + kTok - 1) / kTok + (sp.b1 - sp.b0 + kTok - 1) / kTok;
+}
+
+// The tiles of one KV head and row block in the batch rows before each, and in all,
+// by one warp.
+__device__ __forceinline__ void flat_table(const PartSet& f, int* before) {
+  if (!f.flat) return;
+  const int lane = threadIdx.x & 31;
+  int sum = 0;
+  for (int b0 = 0; b0 < f.n_lens; b0 += 32) {
+    const int b = b0 + lane, mine = b < f.n_lens ? unit_tiles(f, b) : 0;
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (b < f.n_lens) before[b] = sum + x - mine;
+    sum += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (lane == 0) before[f.n_lens] = sum;
+}
+
+// Tiles of all row blocks (below 2^30), and of a group's stretch.
+__device__ __forceinline__ int flat_total(const PartSet& f, const int* before) {
+  return before[f.n_lens] * f.Hkv * f.blocks * f.layers;
+}
+__device__ __forceinline__ int flat_stretch(const PartSet& f, int total) {
+  const int per = (total + kFlatGroups - 1) / kFlatGroups, least = kFlatTiles * f.splits;    // few partials per row
+  return per < least ? least : per;
+}
+
+__device__ __forceinline__ PartRef part_ref(const PartSet& p, const int* before, int u, int r) {
+  PartRef f;
+  f.part = p.part;
+  f.ml = p.ml;
+  f.step = p.row_block;
+  const int v = u * p.blocks + r / p.row_block;
+  if (p.flat) {
+    const int per_b = p.Hkv * p.blocks, b = v / per_b % p.n_lens;
+    const int t = before[b + 1] - before[b], per = flat_stretch(p, flat_total(p, before));
+    const int start = (v / per_b / p.n_lens * before[p.n_lens] + before[b]) * per_b + v % per_b * t;
+    f.n = t ? ((start + t - 1) / per - start / per + 1) * p.splits : 0;
+    f.first = ((size_t)(start / per) + v) * p.splits * p.row_block + r % p.row_block;
+  } else {
+    f.first = (size_t)v * p.splits * p.row_block + r % p.row_block;
+    f.n = p.splits;
+  }
+  return f;
+}
+
+__device__ __forceinline__ PartRef prefix_ref(const DenseAttn& p, const int* before, int u, int r) {
+  const int row = u / p.Hkv, h = u % p.Hkv;
+  return part_ref(p.pre, before, row / p.pre_batch * p.Hkv + h, row % p.pre_batch * p.rows + r);
+}
+
+__device__ __forceinline__ float2 part_ml(const PartRef& f, int s) {
+  return *reinterpret_cast<const float2*>(f.ml + 2 * (f.first + (size_t)s * f.step));
+}
+
+// The largest maximum of a row's partials and m, by one warp.
+__device__ __forceinline__ float parts_max(const PartRef& f, float m) {
+#pragma unroll 4
+  for (int s = threadIdx.x & 31; s < f.n; s += 32) m = fmaxf(m, part_ml(f, s).x);
+  return warp_max(m);
+}
+
+// Add partials s0, s0 + step, ... to a row, by one warp: their sums to l, their
+// accumulators to o, at the maximum mx.  Loads of eight parts are in flight at once.
+template <int D>
+__device__ __forceinline__ void add_parts(const PartRef& f, int s0, int step, float mx, float& l, float (&o)[D / 32]) {
+  const int lane = threadIdx.x & 31;
+  for (int base = s0; base < f.n; base += 32 * step) {
+    const int mine = base + lane * step;
+    const Scales c = scales(mine < f.n ? part_ml(f, mine) : no_part(), mx);
+    l += c.l;
+    const int count = min(32, (f.n - base + step - 1) / step);
+#pragma unroll 8
+    for (int i = 0; i < count; ++i) {
+      float x[D / 32];
+      load_row(f.part + (f.first + (size_t)(base + i * step) * f.step) * D, x);
+      const float a = __shfl_sync(0xffffffffu, c.a, i);
+      const bool none = c.empty >> i & 1u;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) o[k] = fmaf(a, none ? 0.f : x[k], o[k]);
+    }
+  }
+}
+
+// The maximum and sum alone.
+__device__ __forceinline__ float2 parts_ml(const PartRef& f) {
+  const float mx = parts_max(f, -INFINITY);
+  float l = 0.f;
+#pragma unroll 4
+  for (int s = threadIdx.x & 31; s < f.n; s += 32) {
+    const float2 x = part_ml(f, s);
+    if (!empty_part(x.x, x.y)) l = fmaf(part_scale(x.x, mx), x.y, l);
+  }
+  return make_float2(mx, warp_sum(l));
+}
+
+// A merged row to the output, with the shared prefix's partials where there are any.
+template <int D>
+__device__ __forceinline__ void finish_row(const DenseAttn& p, const int* pre_before, int u, int r, float m, float l, float (&o)[D / 32]) {
+  if (p.pre.part) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PartRef f = prefix_ref(p, pre_before, u, r);
+    const float mx = parts_max(f, m);
+    const float a = empty_part(m, l) ? 0.f : part_scale(m, mx);
+    l *= a;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] *= a;
+    add_parts<D>(f, 0, 1, mx, l, o);
+  }
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) o[i] = l == 0.f ? 0.f : o[i] / l;
+  dense_put_row<D>(p, u, r, o);
+}
+
+// What a warp holds of up to 8 NT query rows: queries, running maximum and sum,
+// accumulators.  Columns 2 c4, 2 c4 + 1 of n-tile nt are rows of the row block;
+// rows g, g + 8 of a score tile are tokens.
+//
+// EXACT (fp32 output): the probabilities enter the value product in three bf16
+// parts (24 bits), and each tile's product is formed from zero and added in fp32
+// arithmetic -- the MMA's own accumulation truncates, which over a long context
+// adds up to more than fp32's rounding.  Otherwise two parts (16 bits, well below
+// the output's 8), accumulated by the MMA.
+template <int D, int NT, bool EXACT>
+struct WarpRows {
+  static constexpr int KS = D / 16;      // k-steps of the scores, m-tiles of the values
+  static constexpr int kRowB = 2 * D + 16;               // shared bytes per token row (no bank conflicts)
+  static constexpr int kTileB = kTok * kRowB;
+  uint32_t qb[KS][NT][2];
+  float m_ref[NT][2], l_sum[NT][2], acc[KS][NT][4];
+
+  // queries as B fragments (zero past the block's rows), no tokens seen yet
+  __device__ __forceinline__ void start(const DenseAttn& p, int u, int r0, int n_rows) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g;
+      const __nv_bfloat16* qq = p.q + dense_row_at(p, u, r0 + (r < n_rows ? r : 0));
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {
+        qb[kk][nt][0] = r < n_rows ? *reinterpret_cast<const uint32_t*>(qq + 16 * kk + 2 * c4) : 0u;
+        qb[kk][nt][1] = r < n_rows ? *reinterpret_cast<const uint32_t*>(qq + 16 * kk + 8 + 2 * c4) : 0u;
+      }
+      m_ref[nt][0] = m_ref[nt][1] = -INFINITY;
+      l_sum[nt][0] = l_sum[nt][1] = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.f;
+    }
+  }
+
+  // copy nt tokens' keys and values into a ring stage (rows past them are zero)
+  static __device__ __forceinline__ void issue(uint8_t* st, const DenseAttn& p, int u, int t0, int nt) {
+    constexpr int CPR = D / 8;           // 16-byte chunks per row
+    const int lane = threadIdx.x & 31;
+    const size_t at = ((size_t)u * p.tmax + t0) * (2 * D);
+    const uint8_t* ks = reinterpret_cast<const uint8_t*>(p.k) + at;
+    const uint8_t* vs = reinterpret_cast<const uint8_t*>(p.v) + at;
 #pragma unroll
     for (int x = 0; x < kTok * CPR / 32; ++x) {
       const int c = lane + 32 * x, r = c / CPR, col = c % CPR;
       const int nb = r < nt ? 16 : 0;
       const size_t go = (size_t)(r < nt ? r : 0) * (2 * D) + col * 16;
-      cp_async16(st + r * G::kRowB + col * 16, ks + go, nb);
-      cp_async16(st + G::kTileB + r * G::kRowB + col * 16, vs + go, nb);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < G::kStages - 1; ++i) {
-    if (i < n_mine) issue(i);
-    cp_commit();
-  }
-
-  // queries as B fragments (zero past the block's rows)
-  uint32_t qb[KS][NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = 8 * nt + g;
-    const __nv_bfloat16* qq = p.q + dense_row_at(p, u, r0 + (r < n_rows ? r : 0));
-#pragma unroll
-    for (int kk = 0; kk < KS; ++kk) {
-      qb[kk][nt][0] = r < n_rows ? *reinterpret_cast<const uint32_t*>(qq + 16 * kk + 2 * c4) : 0u;
-      qb[kk][nt][1] = r < n_rows ? *reinterpret_cast<const uint32_t*>(qq + 16 * kk + 8 + 2 * c4) : 0u;
+      cp_async16(st + r * kRowB + col * 16, ks + go, nb);
+      cp_async16(st + kTileB + r * kRowB + col * 16, vs + go, nb);
     }
   }
-  int pos[NT][2];
-  if (MODE == kManyTokens) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) pos[nt][e] = dense_row_pos(p, len, min(r0 + 8 * nt + 2 * c4 + e, p.rows - 1));
-  }
-  float m_ref[NT][2], l_sum[NT][2], acc[KS][NT][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m_ref[nt][0] = m_ref[nt][1] = -INFINITY;
-    l_sum[nt][0] = l_sum[nt][1] = 0.f;
-#pragma unroll
-    for (int mt = 0; mt < KS; ++mt) acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.f;
-  }
 
-  for (int i = 0; i < n_mine; ++i) {
-    if (i + G::kStages - 1 < n_mine) issue(i + G::kStages - 1);
-    cp_commit();
-    cp_wait<G::kStages - 1>();
-    __syncwarp();
-    int t0, nt_tok;
-    tile_at(i, t0, nt_tok);
-    const uint8_t* kt = ring + (i % G::kStages) * (2 * G::kTileB);
-    const uint8_t* vt = kt + G::kTileB;
-    // ---- scores: rows g, g + 8 = tokens; columns 2 c4, 2 c4 + 1 of n-tile nt = query rows
+  // a tile of tokens: mask(s) hides what a row does not see (-inf), then keep(s)
+  // may store the scores (log2 units)
+  template <class Mask, class Keep>
+  __device__ __forceinline__ void tile(const uint8_t* kt, float scale_log2, Mask mask, Keep keep) {
+    const int lane = threadIdx.x & 31;
+    const uint8_t* vt = kt + kTileB;
     float s[NT][4];
     {
       float sb[NT][4];
@@ -172,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(const __grid_co
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) {
         uint32_t a[4];
-        ldmatrix_x4(a, kt + (lane & 15) * G::kRowB + (2 * kk + (lane >> 4)) * 16);
+        ldmatrix_x4(a, kt + (lane & 15) * kRowB + (2 * kk + (lane >> 4)) * 16);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           if (NT < 4 && (kk & 1)) mma_bf16(sb[nt], a, qb[kk][nt][0], qb[kk][nt][1]);
@@ -182,45 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(const __grid_co
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = (NT < 4 ? s[nt][e] + sb[nt][e] : s[nt][e]) * p.scale_log2;
+        for (int e = 0; e < 4; ++e) s[nt][e] = (NT < 4 ? s[nt][e] + sb[nt][e] : s[nt][e]) * scale_log2;
     }
-    if (MODE == kManyTokens) {
-      // a tile that every row sees whole needs no mask
-      const int t1 = t0 + kTok - 1;
-      if (nt_tok < kTok || t1 > p_lo || !(t1 < p.sinks || t0 > p_hi - p.window)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tt = g + 8 * (e >> 1);
-            if (tt >= nt_tok || !sees(t0 + tt, pos[nt][e & 1], p.window, p.sinks)) s[nt][e] = -INFINITY;
-          }
-      }
-    } else if (nt_tok < kTok) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (g + 8 * (e >> 1) >= nt_tok) s[nt][e] = -INFINITY;
-    }
-    if (MODE == kScores) {
-      float* sc = p.scores + ((size_t)u * p.n_tokens + t0) * p.rows + r0;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int tt = g + 8 * h, r = 8 * nt + 2 * c4;
-          if (tt < nt_tok) {
-            float* dst = sc + (size_t)tt * p.rows + r;
-            if (r + 1 < n_rows && (p.rows & 1) == 0) {
-              *reinterpret_cast<float2*>(dst) = make_float2(s[nt][2 * h], s[nt][2 * h + 1]);
-            } else {
-              if (r < n_rows) dst[0] = s[nt][2 * h];
-              if (r + 1 < n_rows) dst[1] = s[nt][2 * h + 1];
-            }
-          }
-        }
-    }
+    mask(s);
+    keep(s);
     // ---- online softmax: the reference maximum is raised only by a score more
     // than 2^8 above it, so that the accumulators are rarely rescaled
     bool need = false;
@@ -266,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(const __grid_co
 #pragma unroll
     for (int mt = 0; mt < KS; ++mt) {
       uint32_t a[4];
-      ldmatrix_x4_trans(a, vt + tok * G::kRowB + (2 * mt + ((lane >> 3) & 1)) * 16);
+      ldmatrix_x4_trans(a, vt + tok * kRowB + (2 * mt + ((lane >> 3) & 1)) * 16);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (EXACT) {
@@ -281,6 +397,133 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(const __grid_co
         }
       }
     }
+  }
+
+  // value e of n-tile nt's rows: the sum over the warp's tokens
+  __device__ __forceinline__ float row_sum(int nt, int e) const {
+    float l = l_sum[nt][e];
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    return l;
+  }
+};
+
+template <int NT>
+__device__ __forceinline__ void mask_past(float (&s)[NT][4], int nt_tok) {
+  const int g = (threadIdx.x & 31) >> 2;
+  if (nt_tok < kTok) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (g + 8 * (e >> 1) >= nt_tok) s[nt][e] = -INFINITY;
+  }
+}
+
+// The mask of several query tokens: rows at positions pos, [p_lo, p_hi] in all.
+template <int NT>
+__device__ __forceinline__ void mask_window(float (&s)[NT][4], const DenseAttn& p, const int (&pos)[NT][2], int p_lo,
+                                            int p_hi, int t0, int nt_tok) {
+  const int g = (threadIdx.x & 31) >> 2, t1 = t0 + kTok - 1;
+  // a tile that every row sees whole needs no mask
+  if (nt_tok == kTok && t1 <= p_lo && (t1 < p.sinks || t0 > p_hi - p.window)) return;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int tt = g + 8 * (e >> 1);
+      if (tt >= nt_tok || !sees(t0 + tt, pos[nt][e & 1], p.window, p.sinks)) s[nt][e] = -INFINITY;
+    }
+}
+
+// ---------------------------------------------------------------- one cluster per row block
+//
+// The latency of small calls: block c of a cluster takes the c-th part of a unit's
+// tokens, its warps every kWarps-th tile of it.
+template <int D, int NT, bool EXACT, int MODE, int SHAPE>
+__global__ void __launch_bounds__(Geo<D, NT, MODE, SHAPE>::kThreads, SHAPE == kSmall ? 2 : 1)
+    dense_attn_kernel(const __grid_constant__ DenseAttn p) {
+  using G = Geo<D, NT, MODE, SHAPE>;
+  constexpr int kWarps = G::kWarps, kThreads = G::kThreads;
+  using W = WarpRows<D, NT, EXACT>;
+  constexpr int RB = 8 * NT, KS = W::KS;
+  extern __shared__ __align__(128) uint8_t dsm[];
+  __shared__ float sm_ml[kWarps][RB][2];
+  __shared__ float2 sm_fin[RB];          // the block's maximum and sum per row
+  __shared__ float2 sm_row[RB];          // the row's maximum and 1 / sum
+  __shared__ int pre_before[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c4 = lane & 3;
+  const int S = p.own.splits;
+  const int split = blockIdx.x % S, ub = blockIdx.x / S;
+  const int u = ub / p.own.blocks, r0 = (ub % p.own.blocks) * RB;
+  const int n_rows = min(RB, p.rows - r0);
+  const int len = dense_len(p, u);
+  // a kernel that merges with this one's partials may start
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // positions of this block's rows (ascending)
+  int p_lo = len - 1, p_hi = len - 1;
+  if (MODE == kManyTokens) p_lo = dense_row_pos(p, len, r0), p_hi = dense_row_pos(p, len, r0 + n_rows - 1);
+  const TokenSpan sp = token_span(p_lo, p_hi, p.window, p.sinks);
+  const int n_a = (sp.a1 + kTok - 1) / kTok;
+  const int n_tiles = n_a + (sp.b1 - sp.b0 + kTok - 1) / kTok;
+  const int per = (n_tiles + S - 1) / S;
+  const int j_end = min(n_tiles, (split + 1) * per);
+  const int j_first = split * per + warp;          // this warp: every kWarps-th tile from here
+  const int n_mine = j_first < j_end ? (j_end - j_first + kWarps - 1) / kWarps : 0;
+  float* const sm_sc = reinterpret_cast<float*>(dsm + G::kSmem);      // scores of the block's tokens, by row
+
+  uint8_t* ring = dsm + warp * G::kWarpB;
+  auto tile_at = [&](int i, int& t0, int& nt) {
+    const int j = j_first + i * kWarps;
+    t0 = j < n_a ? j * kTok : sp.b0 + (j - n_a) * kTok;
+    nt = min(kTok, (j < n_a ? sp.a1 : sp.b1) - t0);
+  };
+  auto issue = [&](int i) {
+    int t0, nt;
+    tile_at(i, t0, nt);
+    W::issue(ring + (i % G::kStages) * (2 * W::kTileB), p, u, t0, nt);
+  };
+#pragma unroll
+  for (int i = 0; i < G::kStages - 1; ++i) {
+    if (i < n_mine) issue(i);
+    cp_commit();
+  }
+  if (p.pre.part && warp == 0) flat_table(p.pre, pre_before);
+  W w;
+  w.start(p, u, r0, n_rows);
+  int pos[NT][2];
+  if (MODE == kManyTokens) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) pos[nt][e] = dense_row_pos(p, len, min(r0 + 8 * nt + 2 * c4 + e, p.rows - 1));
+  }
+  for (int i = 0; i < n_mine; ++i) {
+    if (i + G::kStages - 1 < n_mine) issue(i + G::kStages - 1);
+    cp_commit();
+    cp_wait<G::kStages - 1>();
+    __syncwarp();
+    int t0, nt_tok;
+    tile_at(i, t0, nt_tok);
+    w.tile(
+        ring + (i % G::kStages) * (2 * W::kTileB), p.scale_log2,
+        [&](float (&s)[NT][4]) {
+          if (MODE == kManyTokens) mask_window(s, p, pos, p_lo, p_hi, t0, nt_tok);
+          else mask_past(s, nt_tok);
+        },
+        [&](float (&s)[NT][4]) {
+          if (MODE != kScores) return;
+          const int tok0 = (j_first + i * kWarps - split * per) * kTok;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = 8 * nt + 2 * c4 + (e & 1);
+              if (r < n_rows) sm_sc[r * p.score_stride + tok0 + g + 8 * (e >> 1)] = s[nt][e];
+            }
+        });
     __syncwarp();                        // this stage is refilled next iteration
   }
   cp_wait<0>();
@@ -294,18 +537,16 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(const __grid_co
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float l = l_sum[nt][e];
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      const float l = w.row_sum(nt, e);
       const int r = 8 * nt + 2 * c4 + e;
       float* dst = stage + (warp * RB + r) * RS;
 #pragma unroll
       for (int mt = 0; mt < KS; ++mt) {
-        dst[16 * mt + g] = acc[mt][nt][e];
-        dst[16 * mt + g + 8] = acc[mt][nt][2 + e];
+        dst[16 * mt + g] = w.acc[mt][nt][e];
+        dst[16 * mt + g + 8] = w.acc[mt][nt][2 + e];
       }
       if (g == 0) {
-        sm_ml[warp][r][0] = m_ref[nt][e];
+        sm_ml[warp][r][0] = w.m_ref[nt][e];
         sm_ml[warp][r][1] = l;
       }
     }
@@ -319,172 +560,380 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(const __grid_co
     for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float mw = sm_ml[w][r][0];
-      // a warp without a visible token holds zeros; NaN scores leave mw at
-      // -inf with a NaN sum, which must reach the result
-      const float lw = sm_ml[w][r][1];
-      if (mw == -INFINITY && lw == 0.f) continue;
-      const float a = mw == -INFINITY ? 1.f : exp2f(mw - mx);
+      const float mw = sm_ml[w][r][0], lw = sm_ml[w][r][1];
+      if (empty_part(mw, lw)) continue;
+      const float a = part_scale(mw, mx);
       l = fmaf(a, lw, l);
-      const float* src = stage + (w * RB + r) * RS + lane;
+      float x[D / 32];
+      load_row(stage + (w * RB + r) * RS, x);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(a, src[32 * i], o[i]);
+      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(a, x[i], o[i]);
     }
-    if (p.direct) {
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = l == 0.f ? 0.f : o[i] / l;
-      dense_put_row<D>(p, u, r0 + r, o);
-    } else {
+    if (!p.finish) {
       const size_t at = (size_t)blockIdx.x * RB + r;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) p.part[at * D + lane + 32 * i] = o[i];
-      if (lane == 0) *reinterpret_cast<float2*>(p.ml + 2 * at) = make_float2(mx, l);
+      store_row(p.own.part + at * D, o);
+      if (lane == 0) *reinterpret_cast<float2*>(p.own.ml + 2 * at) = make_float2(mx, l);
+    } else if (S == 1) {
+      if (MODE == kScores && lane == 0) sm_row[r] = make_float2(mx, 1.f / l);
+      finish_row<D>(p, pre_before, u, r0 + r, mx, l, o);
+    } else {
+      // the block's share of the row, over what warp 0 staged (only this warp reads row r)
+      store_row(stage + r * RS, o);
+      if (lane == 0) sm_fin[r] = make_float2(mx, l);
     }
   }
+  if (p.finish && S > 1) {
+    // ---- merge the cluster's blocks: block c takes rows c, c + S, ...
+    cluster_arrive();
+    cluster_wait();
+    for (int r = split + S * warp; r < n_rows; r += S * kWarps) {
+      const Scales c = cluster_scales(&sm_fin[r], S);
+      float o[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+      const uint32_t at = smem_u32(stage + r * RS + lane * (D / 32));
+#pragma unroll 8
+      for (int k = 0; k < S; ++k) {
+        float x[D / 32];
+        ld_cluster_row(map_rank(at, k), x);
+        const float a = __shfl_sync(0xffffffffu, c.a, k);
+        const bool none = c.empty >> k & 1u;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[i] = fmaf(a, none ? 0.f : x[i], o[i]);
+      }
+      finish_row<D>(p, pre_before, u, r0 + r, c.mx, c.l, o);
+    }
+    if (MODE == kScores)
+      for (int r = warp; r < n_rows; r += kWarps) {
+        const Scales c = cluster_scales(&sm_fin[r], S);
+        if (lane == 0) sm_row[r] = make_float2(c.mx, 1.f / c.l);
+      }
+    cluster_arrive();                    // this block reads no other one's memory from here on
+  }
+  if (MODE == kScores) {
+    // ---- weights of the block's tokens
+    __syncthreads();
+    const int t_end = min(len, j_end * kTok), t0 = split * per * kTok;
+    for (int t = t0 + threadIdx.x; t < t_end; t += kThreads) {
+      float* const at = p.weights + (size_t)u * p.tmax + t;
+      const float before = *at;
+      float w = 0.f;
+#pragma unroll 4
+      for (int r = 0; r < n_rows; ++r) {
+        const float2 x = sm_row[r];
+        w = fmaf(exp2f(sm_sc[r * p.score_stride + t - t0] - x.x), x.y, w);
+      }
+      *at = before + w;
+    }
+  }
+  if (p.finish && S > 1) cluster_wait();
+}
+
+// ---------------------------------------------------------------- flat
+//
+// The bandwidth of large calls: the tiles of all units in a row are dealt out to the
+// warps of the grid in equal stretches, whatever the rows' lengths, so that every
+// SM streams the same bytes from start to end; a warp writes a partial for every
+// unit it meets, and a second kernel merges them.
+
+template <int D, int NT, bool EXACT, int MODE>
+__global__ void __launch_bounds__(Geo<D, NT, MODE, kWide>::kThreads, 1)
+    dense_flat_kernel(const __grid_constant__ DenseAttn p) {
+  using G = Geo<D, NT, MODE, kWide>;
+  using W = WarpRows<D, NT, EXACT>;
+  constexpr int RB = 8 * NT, kGroup = G::kWarps;
+  extern __shared__ __align__(128) uint8_t dsm[];
+  __shared__ int before[kMaxBatch + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c4 = lane & 3;
+  const int B = p.own.n_lens;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 0) flat_table(p.own, before);
+  __syncthreads();
+  const int per_b = p.Hkv * p.own.blocks;              // row blocks per batch row
+  const int total = flat_total(p.own, before), per = flat_stretch(p.own, total);
+  const int group = blockIdx.x, member = warp;
+  const int first = min(total, group * per), n = min(per, total - first);
+  if (n <= 0) return;
+
+  // a place in the tiles: row block v of all and its token range, tile j of it
+  struct Place {
+    int v, j, tiles, len, n_a;
+    TokenSpan sp;
+  };
+  auto enter = [&](Place& k) {
+    k.len = dense_len(p, k.v / p.own.blocks);
+    k.sp = token_span(k.len - p.n_q, k.len - 1, p.window, p.sinks);
+    k.n_a = (k.sp.a1 + kTok - 1) / kTok;
+    k.tiles = k.n_a + (k.sp.b1 - k.sp.b0 + kTok - 1) / kTok;
+  };
+  auto tokens = [&](const Place& k, int j, int& t0, int& nt) {
+    t0 = j < k.n_a ? j * kTok : k.sp.b0 + (j - k.n_a) * kTok;
+    nt = min(kTok, (j < k.n_a ? k.sp.a1 : k.sp.b1) - t0);
+  };
+  Place at;
+  {
+    const int per_layer = before[B] * per_b, layer = first / per_layer;
+    const int rest = first % per_layer;                  // within the layer
+    int lo = 0, hi = B - 1;                              // the batch row that holds it
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (before[mid] * per_b <= rest) lo = mid; else hi = mid - 1;
+    }
+    const int in_row = rest - before[lo] * per_b, t = before[lo + 1] - before[lo];
+    at.v = (layer * B + lo) * per_b + in_row / t;
+    enter(at);
+    at.j = in_row % t;
+  }
+  // this warp's tiles of the group's n are member, member + kGroup, ...
+  Place load = at;
+  load.j += member;
+  int i_load = member, stage_load = 0;
+  uint8_t* ring = dsm + warp * G::kWarpB;
+  auto issue = [&]() {
+    if (i_load < n) {
+      while (load.j >= load.tiles) {
+        load.j -= load.tiles;
+        ++load.v;
+        enter(load);
+      }
+      int t0, nt;
+      tokens(load, load.j, t0, nt);
+      W::issue(ring + stage_load * (2 * W::kTileB), p, load.v / p.own.blocks, t0, nt);
+      load.j += kGroup;
+      i_load += kGroup;
+      stage_load = stage_load + 1 == G::kStages ? 0 : stage_load + 1;
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < G::kStages - 1; ++i) issue();
+
+  int i = member, base = -at.j, stage = 0;             // base: where the row block's tiles begin
+  for (;;) {
+    const int u = at.v / p.own.blocks, r0 = at.v % p.own.blocks * RB, n_rows = min(RB, p.rows - r0);
+    W w;
+    w.start(p, u, r0, n_rows);
+    int pos[NT][2];
+    if (MODE == kManyTokens) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) pos[nt][e] = dense_row_pos(p, at.len, min(r0 + 8 * nt + 2 * c4 + e, p.rows - 1));
+    }
+    const int end = min(n, base + at.tiles);
+    for (; i < end; i += kGroup) {
+      issue();
+      cp_wait<G::kStages - 1>();
+      __syncwarp();
+      int t0, nt_tok;
+      tokens(at, i - base, t0, nt_tok);
+      w.tile(
+          ring + stage * (2 * W::kTileB), p.scale_log2,
+          [&](float (&s)[NT][4]) {
+            if (MODE == kManyTokens) mask_window(s, p, pos, at.len - p.n_q, at.len - 1, t0, nt_tok);
+            else mask_past(s, nt_tok);
+          },
+          [&](float (&s)[NT][4]) {
+            if (MODE != kScores) return;
+            float* sc = p.scores + ((size_t)u * p.n_tokens + t0) * p.rows + r0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int tt = g + 8 * h, r = 8 * nt + 2 * c4;
+                if (tt < nt_tok) {
+                  float* dst = sc + (size_t)tt * p.rows + r;
+                  if (r + 1 < n_rows && (p.rows & 1) == 0) {
+                    *reinterpret_cast<float2*>(dst) = make_float2(s[nt][2 * h], s[nt][2 * h + 1]);
+                  } else {
+                    if (r < n_rows) dst[0] = s[nt][2 * h];
+                    if (r + 1 < n_rows) dst[1] = s[nt][2 * h + 1];
+                  }
+                }
+              }
+          });
+      stage = stage + 1 == G::kStages ? 0 : stage + 1;
+      __syncwarp();                      // this stage is refilled next iteration
+    }
+    // the partial of (this warp, row block v)
+    const size_t slot = (((size_t)group + at.v) * kGroup + member) * RB;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float l = w.row_sum(nt, e);
+        const int r = 8 * nt + 2 * c4 + e;
+        if (r < n_rows) {
+          float* dst = p.own.part + (slot + r) * D;
+#pragma unroll
+          for (int mt = 0; mt < W::KS; ++mt) {
+            dst[16 * mt + g] = w.acc[mt][nt][e];
+            dst[16 * mt + g + 8] = w.acc[mt][nt][2 + e];
+          }
+          if (g == 0) *reinterpret_cast<float2*>(p.own.ml + 2 * (slot + r)) = make_float2(w.m_ref[nt][e], l);
+        }
+      }
+    if (end >= n) break;
+    base += at.tiles;
+    do {
+      ++at.v;
+      enter(at);
+    } while (at.tiles == 0);
+  }
+  cp_wait<0>();
 }
 
 // ---------------------------------------------------------------- merge
 
-// Row r's split partials in a set: first index, and how many.
-struct PartRef {
-  const float* part;
-  const float* ml;
-  size_t first;                          // partial of split 0; split s is s * step further
-  int step, n;
-};
+constexpr int kCWarps = 8;
 
-__device__ __forceinline__ PartRef part_ref(const DenseAttn& p, int u, int r) {
-  PartRef f;
-  f.part = p.part;
-  f.ml = p.ml;
-  f.first = ((size_t)u * p.blocks + r / p.row_block) * p.splits * p.row_block + r % p.row_block;
-  f.step = p.row_block;
-  f.n = p.splits;
-  return f;
-}
-
-constexpr int kCWarps = 4;
-
-// The largest maximum and the merged sum of a row's partials, by one warp.
-__device__ __forceinline__ void merge_ml(const PartRef* set, int n_sets, float& mx, float& l) {
-  const int lane = threadIdx.x & 31;
-  mx = -INFINITY;
-  for (int k = 0; k < n_sets; ++k)
-    for (int s = lane; s < set[k].n; s += 32) mx = fmaxf(mx, set[k].ml[2 * (set[k].first + (size_t)s * set[k].step)]);
-  mx = warp_max(mx);
-  l = 0.f;
-  for (int k = 0; k < n_sets; ++k)
-    for (int s = lane; s < set[k].n; s += 32) {
-      const float2 x = *reinterpret_cast<const float2*>(set[k].ml + 2 * (set[k].first + (size_t)s * set[k].step));
-      if (x.x == -INFINITY && x.y == 0.f) continue;
-      l = fmaf(x.x == -INFINITY ? 1.f : exp2f(x.x - mx), x.y, l);
-    }
-  l = warp_sum(l);
-}
-
-// One output row by the kCWarps warps of a block: warp w takes every
-// kCWarps-th partial, then their sums are added.
-template <int D>
-__device__ void merge_row(const DenseAttn& p, int u, int r, const PartRef* set, int n_sets,
-                          float (*red)[D]) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float mx, l, o[D / 32];
-  merge_ml(set, n_sets, mx, l);
+// A row's output from its partials, by WPR warps (the threads of a block hold
+// kCWarps / WPR rows): warp k of a row takes every WPR-th partial.
+template <int D, int WPR>
+__device__ __forceinline__ void merge_row(const DenseAttn& p, const int* before, const int* pre_before, int u, int r, bool has,
+                                          float (*red)[D]) {
+  const int warp = threadIdx.x >> 5, k = warp % WPR;
+  float l = 0.f, o[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-  for (int k = 0; k < n_sets; ++k)
-#pragma unroll 4
-    for (int s = warp; s < set[k].n; s += kCWarps) {
-      const size_t at = set[k].first + (size_t)s * set[k].step;
-      const float2 x = *reinterpret_cast<const float2*>(set[k].ml + 2 * at);
-      if (x.x == -INFINITY && x.y == 0.f) continue;
-      const float a = x.x == -INFINITY ? 1.f : exp2f(x.x - mx);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(a, set[k].part[at * D + lane + 32 * i], o[i]);
+  if (has) {
+    const PartRef own = part_ref(p.own, before, u, r);
+    float mx = parts_max(own, -INFINITY);
+    if (p.pre.part) {
+      const PartRef pre = prefix_ref(p, pre_before, u, r);
+      mx = parts_max(pre, mx);
+      add_parts<D>(pre, k, WPR, mx, l, o);
     }
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) red[warp][lane + 32 * i] = o[i];
-  __syncthreads();
-  if (warp == 0) {
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      float t = 0.f;
-#pragma unroll
-      for (int w = 0; w < kCWarps; ++w) t += red[w][lane + 32 * i];
-      o[i] = l == 0.f ? 0.f : t / l;
-    }
-    dense_put_row<D>(p, u, r, o);
+    add_parts<D>(own, k, WPR, mx, l, o);
   }
-}
-
-template <int D>
-__global__ void __launch_bounds__(32 * kCWarps) dense_combine_kernel(const __grid_constant__ DenseAttn p,
-                                                                     const __grid_constant__ DenseAttn pre,
-                                                                     int has_prefix) {
-  __shared__ float red[kCWarps][D];
-  const int u = blockIdx.x / p.rows, r = blockIdx.x % p.rows;
-  PartRef set[2];
-  set[0] = part_ref(p, u, r);
-  if (has_prefix) {
-    // the prefix's unit is the KV head, its rows run over the batch's rows too
-    const int row = u / p.Hkv, batch = p.units / pre.units, h = u % p.Hkv;
-    set[1] = part_ref(pre, (row / batch) * p.Hkv + h, (row % batch) * p.rows + r);
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  merge_row<D>(p, u, r, set, has_prefix ? 2 : 1, red);
-}
-
-// Blocks of unit u: block c < rows merges output row c (and further rows in
-// turn where there are more rows than blocks); every block adds the weights of
-// its tokens.
-constexpr int kAccTok = 1024;            // tokens per block
-
-template <int D>
-__global__ void __launch_bounds__(32 * kCWarps) dense_accum_kernel(const __grid_constant__ DenseAttn p,
-                                                                   float* weights, int chunks) {
-  extern __shared__ float2 sm_row[];     // per row: maximum, 1 / sum
-  __shared__ float red[kCWarps][D];
-  const int u = blockIdx.x / chunks, c = blockIdx.x % chunks;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int r = c; r < p.rows; r += chunks) {
-    const PartRef set = part_ref(p, u, r);
-    merge_row<D>(p, u, r, &set, 1, red);
+  if (WPR > 1) {
+    __shared__ float sum[kCWarps];
+    store_row(red[warp], o);
+    if ((threadIdx.x & 31) == 0) sum[warp] = l;
     __syncthreads();
+    if (k) return;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) {
+      float x[D / 32];
+      load_row(red[warp + w], x);
+      l += sum[warp + w];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) o[i] += x[i];
+    }
   }
-  const int len = dense_len(p, u);
-  if (c * kAccTok >= len) return;
-  for (int r = warp; r < p.rows; r += kCWarps) {
-    const PartRef set = part_ref(p, u, r);
-    float mx, l;
-    merge_ml(&set, 1, mx, l);
-    if (lane == 0) sm_row[r] = make_float2(mx, 1.f / l);
+  if (!has) return;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) o[i] = l == 0.f ? 0.f : o[i] / l;
+  dense_put_row<D>(p, u, r, o);
+}
+
+template <int D, int WPR>
+__global__ void __launch_bounds__(32 * kCWarps) dense_combine_kernel(const __grid_constant__ DenseAttn p) {
+  __shared__ float red[WPR > 1 ? kCWarps : 1][D];
+  const long long row = (long long)blockIdx.x * (kCWarps / WPR) + (threadIdx.x >> 5) / WPR;
+  const bool has = row < (long long)p.units * p.rows;
+  __shared__ int before[kMaxBatch + 1], pre_before[2];
+  if (threadIdx.x < 32) {
+    flat_table(p.own, before);
+    if (p.pre.part) flat_table(p.pre, pre_before);
   }
   __syncthreads();
-  const int end = min(len, (c + 1) * kAccTok);
-  for (int t = c * kAccTok + threadIdx.x; t < end; t += 32 * kCWarps) {
-    const float* sc = p.scores + ((size_t)u * p.n_tokens + t) * p.rows;
-    float w = 0.f;
-    for (int r = 0; r < p.rows; ++r) {
-      const float2 x = sm_row[r];
-      w = fmaf(exp2f(sc[r] - x.x), x.y, w);
-    }
-    weights[(size_t)u * p.tmax + t] += w;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  merge_row<D, WPR>(p, before, pre_before, has ? (int)(row / p.rows) : 0, (int)(row % p.rows), has, red);
+}
+
+// Blocks of a unit: `merges` blocks merge its output rows, the others add the
+// weights of kAccTok tokens each.
+constexpr int kAccTok = 1024;
+
+template <int D, int WPR>
+__global__ void __launch_bounds__(32 * kCWarps) dense_accum_kernel(const __grid_constant__ DenseAttn p, int merges,
+                                                                   int blocks) {
+  constexpr int PT = kAccTok / (32 * kCWarps);           // tokens per thread
+  extern __shared__ float2 sm_row[];     // per row: maximum, 1 / sum
+  __shared__ float red[WPR > 1 ? kCWarps : 1][D];
+  const int u = blockIdx.x / blocks, c = blockIdx.x % blocks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int len = dense_len(p, u), t0 = (c - merges) * kAccTok + threadIdx.x;
+  __shared__ int before[kMaxBatch + 1];
+  if (warp == 0) flat_table(p.own, before);
+  __syncthreads();
+  if (c < merges) {
+    const int r = c * (kCWarps / WPR) + warp / WPR;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    merge_row<D, WPR>(p, before, nullptr, u, r, r < p.rows, red);
+    return;
   }
+  if (t0 - (int)threadIdx.x >= len) return;
+  float* const at = p.weights + (size_t)u * p.tmax + t0;
+  const float* const sc = p.scores + ((size_t)u * p.n_tokens + t0) * p.rows;
+  float w[PT], old[PT];
+  bool has[PT];
+#pragma unroll
+  for (int k = 0; k < PT; ++k) {
+    has[k] = t0 + 32 * kCWarps * k < len;
+    old[k] = has[k] ? at[32 * kCWarps * k] : 0.f;
+    w[k] = 0.f;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int r = warp; r < p.rows; r += kCWarps) {
+    const float2 x = parts_ml(part_ref(p.own, before, u, r));
+    if (lane == 0) sm_row[r] = make_float2(x.x, 1.f / x.y);
+  }
+  const size_t step = (size_t)32 * kCWarps * p.rows;
+  if (p.rows % 4 == 0) {
+    float4 x[PT];                        // the first rows' scores are on their way before the row sums are known
+    auto load = [&](int r) {
+#pragma unroll
+      for (int k = 0; k < PT; ++k)
+        x[k] = has[k] ? *reinterpret_cast<const float4*>(sc + k * step + r) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);
+    __syncthreads();
+    for (int r = 0; r < p.rows; r += 4) {
+      if (r) load(r);
+      const float2 a = sm_row[r], b = sm_row[r + 1], e = sm_row[r + 2], f = sm_row[r + 3];
+#pragma unroll
+      for (int k = 0; k < PT; ++k) {
+        w[k] = fmaf(exp2f(x[k].x - a.x), a.y, w[k]);
+        w[k] = fmaf(exp2f(x[k].y - b.x), b.y, w[k]);
+        w[k] = fmaf(exp2f(x[k].z - e.x), e.y, w[k]);
+        w[k] = fmaf(exp2f(x[k].w - f.x), f.y, w[k]);
+      }
+    }
+  } else {
+    __syncthreads();
+    for (int r = 0; r < p.rows; ++r) {
+      const float2 a = sm_row[r];
+#pragma unroll
+      for (int k = 0; k < PT; ++k) w[k] = fmaf(exp2f((has[k] ? sc[k * step + r] : a.x) - a.x), a.y, w[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < PT; ++k)
+    if (has[k]) at[32 * kCWarps * k] = old[k] + w[k];
 }
 
 template <int D, int NT, bool EXACT, int MODE>
 cudaError_t launch_one(const DenseAttn& p, cudaLaunchConfig_t& cfg) {
-  auto* f = dense_attn_kernel<D, NT, EXACT, MODE>;
-  const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
-  if (e != cudaSuccess) return e;
-  cfg.dynamicSmemBytes = Geo<D>::kSmem;
-  return cudaLaunchKernelEx(&cfg, f, p);
+  using S = Geo<D, NT, MODE, kSmall>;
+  using W = Geo<D, NT, MODE, kWide>;
+  auto* f = dense_attn_kernel<D, NT, EXACT, MODE, kSmall>;
+  cfg.blockDim = dim3(p.own.flat || p.wide ? W::kThreads : S::kThreads);
+  cfg.dynamicSmemBytes =
+      p.own.flat || p.wide ? W::kSmem : S::kSmem + (size_t)(p.score_stride * p.rows) * sizeof(float);
+  if (p.own.flat) f = dense_flat_kernel<D, NT, EXACT, MODE>;
+  else if (p.wide && MODE != kScores) f = dense_attn_kernel<D, NT, EXACT, MODE == kScores ? kOneToken : MODE, kWide>;
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess && !p.own.flat && p.finish && p.own.splits > 8)
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, f, p);
 }
 
 template <int D, int NT>
 cudaError_t launch_nt(const DenseAttn& p, cudaLaunchConfig_t& cfg) {
-  const int mode = p.scores ? kScores : p.n_q > 1 ? kManyTokens : kOneToken;
+  const int mode = p.weights ? kScores : p.n_q > 1 ? kManyTokens : kOneToken;
   if (p.out_bf16) {
     if (mode == kScores) return launch_one<D, NT, false, kScores>(p, cfg);
     if (mode == kManyTokens) return launch_one<D, NT, false, kManyTokens>(p, cfg);
@@ -497,29 +946,61 @@ cudaError_t launch_nt(const DenseAttn& p, cudaLaunchConfig_t& cfg) {
 
 template <int D>
 cudaError_t launch_d(const DenseAttn& p, cudaLaunchConfig_t& cfg) {
-  if (p.row_block == 8) return launch_nt<D, 1>(p, cfg);
-  if (p.row_block == 16) return launch_nt<D, 2>(p, cfg);
+  if (p.own.row_block == 8) return launch_nt<D, 1>(p, cfg);
+  if (p.own.row_block == 16) return launch_nt<D, 2>(p, cfg);
   return launch_nt<D, 4>(p, cfg);
+}
+
+// Partials of a flat plan: one per warp of every (group, row block) that meet; at
+// least kFlatTiles tiles of 16 tokens per warp.
+long long flat_slots(long long blocks, long long tokens) {
+  const long long parts = tokens > 64 ? blocks * ((tokens + 63) / 64) : blocks;
+  return (blocks + (parts < kFlatGroups ? parts : kFlatGroups)) * 16;
+}
+
+// Warps that share a row block's tiles in the flat kernel.
+int flat_splits(int row_block, int d) {
+  return row_block == 8 && d == 64 ? Geo<64, 1, kOneToken, kWide>::kWarps : Geo<128, 1, kOneToken, kWide>::kWarps;
+}
+
+int warp_row_block(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+
+// Splits of `blocks` row blocks over clusters, at least one tile per warp each.
+int warp_splits(long long blocks, long long tokens) {
+  const long long most = (tokens + 63) / 64;
+  long long best = 1;
+  double best_fill = 0.;
+  for (long long s = 1; s <= most && s <= kMaxCluster; ++s) {
+    const long long waves = (blocks * s + kSlots - 1) / kSlots;
+    const double fill = (double)(blocks * s) / (double)(waves * kSlots);
+    if (fill > best_fill + 0.02) best = s, best_fill = fill;
+    if (fill >= 0.85 || blocks * s > kWaves * kSlots) break;
+  }
+  return (int)best;
 }
 
 }  // namespace
 
-// The kernel and the split of a problem's tokens.
-//
-// Warp-level kernel: blocks of up to 32 rows, one block per SM at a time; enough
-// splits for every SM, none with fewer tiles than warps; where the blocks alone
-// exceed the SMs, as few splits as fill whole waves to nine tenths.
+// The kernel and the split of a problem's tokens (group: query rows per token).
 //
 // tcgen05 kernel: bf16 output and at least kTensorRows rows per KV head.  256 rows
 // per block where rows and tokens give every SM a block, 128 otherwise; splits of
 // at least two tiles per score stream up to one block per SM.
-DensePlan dense_plan(int units, int rows, long long tokens, int out_bf16) {
-  DensePlan f;
+//
+// Warp-level kernels: blocks of up to 32 rows.  Wide blocks take long rows where one
+// block each fills the SMs once (104 to 148; batch 16 at 64K, window 8192: 88 us, 94
+// in two clustered halves, 101 flat and merged).  Fewer row blocks, or a merge that is
+// there anyway: the tiles are dealt out flat from `flat_from` of 8 KB (where the row
+// blocks of a unit see the same tokens).  Else clusters of up to kMaxCluster blocks,
+// or of one (256 to 1024 short rows behind a prefix: 45 and 137 us, 61 and 153 flat).
+DensePlan dense_plan(int units, int group, int n_q, int d, long long tokens, int out_bf16, int flat_from) {
+  DensePlan f = {};
+  const long long rows = (long long)group * n_q;
   if (out_bf16 && rows >= kTensorRows) {
     const long long tiles = (tokens + 127) / 128, wide = (long long)units * ((rows + 255) / 256);
     f.tensor = 1;
     f.row_block = rows > 128 && wide * (tiles / 2 > 1 ? tiles / 2 : 1) >= kNumSMs ? 256 : 128;
-    f.blocks = (rows + f.row_block - 1) / f.row_block;
+    f.blocks = (int)((rows + f.row_block - 1) / f.row_block);
     const long long ctas = (long long)units * f.blocks, most = tiles / (f.row_block == 256 ? 2 : 4);
     long long s = kNumSMs / ctas;
     s = s < most ? s : most;
@@ -528,83 +1009,131 @@ DensePlan dense_plan(int units, int rows, long long tokens, int out_bf16) {
       s = (tiles + per - 1) / per;
     }
     f.splits = s > 1 ? (int)s : 1;
+    f.slots = ctas * f.splits;
     return f;
   }
-  f.tensor = 0;
-  f.row_block = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-  f.blocks = (rows + f.row_block - 1) / f.row_block;
-  const long long blocks = (long long)units * f.blocks;
-  const long long most = (tokens + kTok * kWarps - 1) / (kTok * kWarps);
-  long long best = 1;
-  double best_fill = 0.;
-  for (long long s = 1; s <= most && s <= kNumSMs; ++s) {
-    const long long waves = (blocks * s + kNumSMs - 1) / kNumSMs;
-    const double fill = (double)(blocks * s) / (double)(waves * kNumSMs);
-    if (fill > best_fill + 0.02) best = s, best_fill = fill;
-    if (fill >= 0.9 || blocks * s > kWaves * kNumSMs) break;
+  f.row_block = warp_row_block(rows);
+  f.blocks = (int)((rows + f.row_block - 1) / f.row_block);
+  const long long nb = (long long)units * f.blocks, tiles = (tokens + kTok - 1) / kTok;
+  f.wide = flat_from > kFlatMerge && nb >= 104 && nb <= kNumSMs && tiles >= 128;
+  f.flat = !f.wide && (nb < 104 || flat_from == kFlatMerge) && (n_q == 1 || f.blocks == 1) && nb * tiles * d / 128 >= flat_from && nb * (tiles + 1) < 1 << 30;
+  f.splits = f.wide ? 1 : f.flat ? flat_splits(f.row_block, d) : warp_splits(nb, tokens);
+  f.slots = f.flat ? flat_slots(nb, tokens) : nb * f.splits;
+  return f;
+}
+
+// Scores in shared memory: one row block per unit, as many splits as the SMs ask for
+// and as leave 32 KB of scores per block, so that two blocks run per SM; else flat.
+DensePlan dense_accum_plan(int units, int rows, int d, long long tokens, int* score_stride) {
+  DensePlan f = dense_plan(units, rows, 1, d, tokens, 0, kFlatMerge);
+  *score_stride = 0;
+  if (f.flat) return f;
+  // floats per row: whole tiles, 4 mod 32 (the rows of a fragment fall into different banks)
+  auto stride = [&](long long s) {
+    const long long tiles = ((tokens + kTok - 1) / kTok + s - 1) / s;
+    return (tiles * kTok + 31) / 32 * 32 + 4;
+  };
+  long long s = f.splits;
+  while (s < kMaxCluster && stride(s) * rows * 4 > 32 * 1024) ++s;
+  if (f.blocks > 1 || stride(s) * rows * 4 > 32 * 1024) {
+    f.flat = 1;
+    f.splits = flat_splits(f.row_block, d);
+    f.slots = flat_slots((long long)units * f.blocks, tokens);
+  } else {
+    f.splits = (int)s;
+    *score_stride = (int)stride(s);
   }
-  f.splits = (int)best;
   return f;
 }
 
 // Row slots that the partials take in any call of up to `tokens` tokens and, with
-// `direct`, of up to `rows` rows (a call of one split then writes its output and
-// needs none).
-long long dense_part_rows(long long units, long long rows, long long tokens, int out_bf16, bool direct) {
-  const long long tiles = tokens > 128 ? (tokens + 127) / 128 : 1;
-  if (out_bf16 && rows >= kTensorRows) {
+// `direct`, of up to n_q query tokens (one split, or a cluster, then writes the
+// output and needs none).
+long long dense_part_rows(long long units, long long group, long long n_q, long long tokens, int out_bf16,
+                          bool direct) {
+  const long long rows = group * n_q;
+  long long n = 0;
+  const bool tensor = out_bf16 && rows >= kTensorRows;
+  if (tensor) {
     // splits only while the blocks do not fill the SMs
-    const long long wide = units * ((rows + 255) / 256);
-    if (wide >= kNumSMs && !direct) return wide * 256;
-    return 256 * (wide * tiles < kNumSMs ? wide * tiles : kNumSMs);
+    const long long wide = units * ((rows + 255) / 256), tiles = tokens > 128 ? (tokens + 127) / 128 : 1;
+    n = 256 * (wide * tiles < kNumSMs ? wide * tiles : kNumSMs);
+    if (wide >= kNumSMs && !direct) n = wide * 256;
   }
-  // splits until the blocks pass kWaves waves, and none where they do without
-  const int rb = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-  const long long nb = units * ((rows + rb - 1) / rb);
-  if (nb > kWaves * kNumSMs && !direct) return nb * rb;
-  const long long most = (nb < kWaves * kNumSMs ? nb : kWaves * kNumSMs) + kWaves * kNumSMs;
-  return rb * (nb * tiles < most ? nb * tiles : most);
+  if (!tensor || direct) {
+    // a cluster plan has no more; a flat one of several query tokens has one row block
+    const long long most = n_q == 1 || rows <= 32 ? rows : group > 32 ? group : 32;
+    const int rb = warp_row_block(most);
+    const long long m = rb * flat_slots(units * ((most + rb - 1) / rb), tokens);
+    n = n > m ? n : m;
+  }
+  return n;
 }
 
-cudaError_t launch_dense_attn(const DenseAttn& p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)p.units * p.blocks * p.splits));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
+static void dependent_launch(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr) {
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = cfg.attrs ? cfg.attrs : attr;
+  ++cfg.numAttrs;
+}
+
+cudaError_t launch_dense_attn(const DenseAttn& p, cudaStream_t s, bool dependent) {
   if (p.tensor) return launch_dense_attn_tc(p, s);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(p.own.flat ? kFlatGroups : (unsigned)((long long)p.units * p.own.blocks * p.own.splits));
+  cfg.stream = s;
+  if (!p.own.flat && p.finish && p.own.splits > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.own.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  if (dependent) dependent_launch(cfg, attr + cfg.numAttrs);
   return p.d == 128 ? launch_d<128>(p, cfg) : launch_d<64>(p, cfg);
 }
 
-static void dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr) {
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+// More than 32 partials per row are merged by a block of warps.
+static bool many_parts(const DenseAttn& p) {
+  auto parts = [](const PartSet& f, long long units) {
+    return f.flat ? (kFlatGroups / (units * f.blocks) + 2) * f.splits : (long long)f.splits;
+  };
+  return parts(p.own, p.units) > 32 || (p.pre.part && parts(p.pre, p.units / p.pre_batch) > 32);
 }
 
-cudaError_t launch_dense_combine(const DenseAttn& p, const DenseAttn* prefix, cudaStream_t s) {
+cudaError_t launch_dense_combine(const DenseAttn& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3((unsigned)((long long)p.units * p.rows));
+  cudaLaunchAttribute attr;
+  const bool many = many_parts(p);
+  const long long rows = (long long)p.units * p.rows;
+  cfg.gridDim = dim3((unsigned)(many ? rows : (rows + kCWarps - 1) / kCWarps));
   cfg.blockDim = dim3(32 * kCWarps);
   cfg.stream = s;
-  dependent(cfg, attr);
-  const DenseAttn& pre = prefix ? *prefix : p;
-  if (p.d == 128) return cudaLaunchKernelEx(&cfg, dense_combine_kernel<128>, p, pre, prefix ? 1 : 0);
-  return cudaLaunchKernelEx(&cfg, dense_combine_kernel<64>, p, pre, prefix ? 1 : 0);
+  dependent_launch(cfg, &attr);
+  if (p.d == 128)
+    return many ? cudaLaunchKernelEx(&cfg, dense_combine_kernel<128, kCWarps>, p)
+                : cudaLaunchKernelEx(&cfg, dense_combine_kernel<128, 1>, p);
+  return many ? cudaLaunchKernelEx(&cfg, dense_combine_kernel<64, kCWarps>, p)
+              : cudaLaunchKernelEx(&cfg, dense_combine_kernel<64, 1>, p);
 }
 
-cudaError_t launch_dense_accum(const DenseAttn& p, float* weights, cudaStream_t s) {
+cudaError_t launch_dense_accum(const DenseAttn& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  const int chunks = (p.n_tokens + kAccTok - 1) / kAccTok;
-  cfg.gridDim = dim3((unsigned)((long long)p.units * (chunks > 0 ? chunks : 1)));
+  cudaLaunchAttribute attr;
+  const bool many = many_parts(p);
+  const int merges = many ? p.rows : (p.rows + kCWarps - 1) / kCWarps;
+  const int blocks = merges + (p.n_tokens + kAccTok - 1) / kAccTok;
+  cfg.gridDim = dim3((unsigned)((long long)p.units * blocks));
   cfg.blockDim = dim3(32 * kCWarps);
   cfg.dynamicSmemBytes = (size_t)p.rows * sizeof(float2);
   cfg.stream = s;
-  dependent(cfg, attr);
-  if (p.d == 128) return cudaLaunchKernelEx(&cfg, dense_accum_kernel<128>, p, weights, chunks > 0 ? chunks : 1);
-  return cudaLaunchKernelEx(&cfg, dense_accum_kernel<64>, p, weights, chunks > 0 ? chunks : 1);
+  dependent_launch(cfg, &attr);
+  if (p.d == 128)
+    return many ? cudaLaunchKernelEx(&cfg, dense_accum_kernel<128, kCWarps>, p, merges, blocks)
+                : cudaLaunchKernelEx(&cfg, dense_accum_kernel<128, 1>, p, merges, blocks);
+  return many ? cudaLaunchKernelEx(&cfg, dense_accum_kernel<64, kCWarps>, p, merges, blocks)
+              : cudaLaunchKernelEx(&cfg, dense_accum_kernel<64, 1>, p, merges, blocks);
 }
 
 }  // namespace kvc

@@ -142,17 +142,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* const sm_q = dsm;
   uint8_t* const ring = dsm + 2 * C::kTileB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x % p.splits, ub = blockIdx.x / p.splits;
-  const int u = ub / p.blocks, r0 = (ub % p.blocks) * RB;
+  const int split = blockIdx.x % p.own.splits, ub = blockIdx.x / p.own.splits;
+  const int u = ub / p.own.blocks, r0 = (ub % p.own.blocks) * RB;
   const int n_rows = min(RB, p.rows - r0);
   const int len = dense_len(p, u);
+  // a kernel that merges with this one's partials may start
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int p_lo = dense_row_pos(p, len, r0), p_hi = dense_row_pos(p, len, r0 + n_rows - 1);
   Tiles tl;
   tl.sp = token_span(p_lo, p_hi, p.window, p.sinks);
   tl.n_a = (tl.sp.a1 + kTN - 1) / kTN;
   {
     const int all = tl.n_a + (tl.sp.b1 - tl.sp.b0 + kTN - 1) / kTN;
-    const int per = (all + p.splits - 1) / p.splits;
+    const int per = (all + p.own.splits - 1) / p.own.splits;
     tl.first = min(all, split * per);
     tl.n = min(all, tl.first + per) - tl.first;
   }
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (other) f[i] = fmaf(a1, stage[(c + i) * kTM + row], f[i]);
           if (l == 0.f) f[i] = 0.f;
         }
-        if (p.direct) {
+        if (p.finish) {
           uint32_t w[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -481,12 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
           }
         } else if (r < n_rows) {
-          float4* dst = reinterpret_cast<float4*>(p.part + at * D + c);
+          float4* dst = reinterpret_cast<float4*>(p.own.part + at * D + c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
         }
       }
-      if (p.direct) {
+      if (p.finish) {
         // rows that another row's NaN or infinity may have reached: from the definition
         if (p.n_q > 1) {
           unsigned bad = __ballot_sync(0xffffffffu, !fine && r < n_rows);
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else if (r < n_rows) {
-        *reinterpret_cast<float2*>(p.ml + 2 * at) = make_float2(m_ref, l);
+        *reinterpret_cast<float2*>(p.own.ml + 2 * at) = make_float2(m_ref, l);
       }
     }
   }
@@ -544,14 +546,14 @@ cudaError_t launch(const DenseAttn& p, cudaStream_t s) {
   auto* f = dense_attn_tc_kernel<D, PAIR>;
   e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  f<<<(unsigned)((long long)p.units * p.blocks * p.splits), kThreads, Cfg<D>::kSmem, s>>>(p, mk, mv);
+  f<<<(unsigned)((long long)p.units * p.own.blocks * p.own.splits), kThreads, Cfg<D>::kSmem, s>>>(p, mk, mv);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_dense_attn_tc(const DenseAttn& p, cudaStream_t s) {
-  const bool pair = p.row_block == 2 * kTM;
+  const bool pair = p.own.row_block == 2 * kTM;
   if (p.d == 128) return pair ? launch<128, true>(p, s) : launch<128, false>(p, s);
   return pair ? launch<64, true>(p, s) : launch<64, false>(p, s);
 }

@@ -80,23 +80,81 @@ bool too_large(long long units, long long rows) {
 
 // Bytes of the partials of a problem, for all layers of a layout or one of them
 // (one alone may split further).
-size_t part_bytes(const kvc_layout* L, long long units, long long rows, long long tokens, bool bf16, bool direct) {
-  long long n = kvc::dense_part_rows(units * L->L, rows, tokens, bf16, direct);
-  const long long one = kvc::dense_part_rows(units, rows, tokens, bf16, direct);
+size_t part_bytes(const kvc_layout* L, long long units, long long group, long long n_q, long long tokens, bool bf16,
+                  bool direct) {
+  long long n = kvc::dense_part_rows(units * L->L, group, n_q, tokens, bf16, direct);
+  const long long one = kvc::dense_part_rows(units, group, n_q, tokens, bf16, direct);
   if (one > n) n = one;
   return round_up((size_t)n * L->d.head_dim * 4, 256) + round_up((size_t)n * 8, 256);
 }
 
-// Fill in the split plan over `tokens` tokens and place the partials at `at`.
-void place_parts(kvc::DenseAttn* p, long long tokens, char* at) {
-  const kvc::DensePlan f = kvc::dense_plan(p->units, p->rows, tokens, p->out_bf16 && !p->scores);
+// Take a split plan and place its partials at `at`.  One split writes the output unless its partials are asked for, and so does
+// a cluster of warp-level blocks.  Returns where the partials end.
+char* take_plan(kvc::DenseAttn* p, const kvc::DensePlan& f, bool partials, char* at) {
   p->tensor = p->clear_err = f.tensor;
-  p->row_block = f.row_block;
-  p->blocks = f.blocks;
-  p->splits = f.splits;
-  const size_t n = (size_t)p->units * p->blocks * p->splits * p->row_block;
-  p->part = (float*)at;
-  p->ml = (float*)(at + round_up(n * p->d * 4, 256));
+  p->own.row_block = f.row_block;
+  p->own.blocks = f.blocks;
+  p->own.splits = f.splits;
+  p->wide = f.wide;
+  p->own.flat = f.flat;
+  p->own.Hkv = p->Hkv;
+  p->own.layers = p->units / (p->Hkv * p->len_rows);
+  p->own.lens = p->seq_lens;
+  p->own.n_lens = p->len_rows;
+  p->own.n_tokens = p->n_tokens;
+  p->own.n_q = p->n_q;
+  p->own.window = p->window;
+  p->own.sinks = p->sinks;
+  p->finish = !partials && (f.tensor ? f.splits == 1 : !f.flat);
+  const size_t n = p->finish ? 0 : (size_t)f.slots * f.row_block;
+  p->own.part = (float*)at;
+  p->own.ml = (float*)(at + round_up(n * p->d * 4, 256));
+  return (char*)p->own.ml + n * 8;
+}
+
+// The three calls' plans, placed in the workspace; each returns the end of what it uses.
+
+char* plan_window(const kvc_layout* L, kvc::DenseAttn* p, int window, int sinks, void* ws) {
+  if (window < p->window) p->window = window;
+  p->sinks = sinks < p->tmax ? sinks : p->tmax;
+  p->err = (uint32_t*)ws;
+  // tokens that a block of rows reads, for the split (a block is at most 256 rows)
+  const int at_once = L->G < 256 ? 256 / L->G : 1;
+  long long span = (long long)p->window + p->sinks + (p->n_q < at_once ? p->n_q : at_once) - 1;
+  if (span > p->n_tokens) span = p->n_tokens;
+  return take_plan(p, kvc::dense_plan(p->units, L->G, p->n_q, p->d, span, p->out_bf16, kvc::kFlatFrom), false, (char*)ws + kHeader);
+}
+
+char* plan_accum(kvc::DenseAttn* p, void* ws) {
+  p->err = (uint32_t*)ws;
+  char* at = (char*)ws + kHeader;
+  p->scores = (float*)at;
+  at += round_up((size_t)p->units * p->rows * (size_t)p->n_tokens * 4, 256);
+  return take_plan(p, kvc::dense_accum_plan(p->units, p->rows, p->d, p->n_tokens, &p->score_stride), false, at);
+}
+
+char* plan_prefix(const kvc_layout* L, kvc::DenseAttn* p, kvc::DenseAttn* pre, void* ws) {
+  p->err = pre->err = (uint32_t*)ws;
+  // the prefix's rows: every query head of the KV head's group, of every batch row
+  pre->out_bf16 = p->out_bf16;
+  pre->rows = L->d.batch * L->G;
+  pre->r_div = L->G;
+  pre->q_hi = p->q_row;
+  pre->q_row = p->q_row * L->d.batch;
+  pre->q_head = p->q_head;
+  char* at = (char*)ws + kHeader;
+  const kvc::DensePlan f = kvc::dense_plan(p->units, L->G, 1, p->d, p->n_tokens, p->out_bf16, kvc::kFlatFrom);
+  take_plan(p, f, f.tensor, at);                  // the tcgen05 kernel does not merge with the prefix
+  at += part_bytes(L, (long long)L->d.batch * p->Hkv, L->G, 1, p->n_tokens, p->out_bf16, false);
+  char* const end = take_plan(pre, kvc::dense_plan(pre->units, pre->rows, 1, p->d, pre->n_tokens, p->out_bf16, kvc::kFlatMerge), true, at);
+  p->pre = pre->own;
+  p->pre_batch = L->d.batch;
+  return end;
+}
+
+kvc_status check_end(const char* what, const void* ws, size_t size, const char* end) {
+  const size_t used = (size_t)(end - (const char*)ws);
+  return used <= size ? KVC_OK : report_error(KVC_EWORKSPACE, "%s: workspace %zu bytes < %zu used", what, size, used);
 }
 
 }  // namespace
@@ -105,7 +163,7 @@ extern "C" size_t kvc_window_workspace_bytes(const kvc_layout* L, int32_t n_toke
   if (!L || L->d.kind != KVC_DENSE_BF16 || n_q < 1) return 0;
   const long long units = (long long)L->d.batch * L->d.n_kv_heads, rows = (long long)L->G * n_q;
   if (too_large(units * L->L, rows)) return 0;
-  return kHeader + part_bytes(L, units, rows, n_tokens, L->d.out_bf16, true);
+  return kHeader + part_bytes(L, units, L->G, n_q, n_tokens, L->d.out_bf16, true);
 }
 
 extern "C" kvc_status kvc_window_attn(const kvc_layout* L, const kvc_cache* c, const void* q, int32_t n_q,
@@ -125,27 +183,20 @@ extern "C" kvc_status kvc_window_attn(const kvc_layout* L, const kvc_cache* c, c
   if ((st = check_ws(what, workspace, ws_size, kvc_window_workspace_bytes(L, c->n_tokens, n_q))) != KVC_OK) return st;
   p.q = (const __nv_bfloat16*)q;
   p.out = out;
-  if (window < p.window) p.window = window;
-  p.sinks = sinks < p.tmax ? sinks : p.tmax;
-  p.err = (uint32_t*)workspace;
-  // tokens that a block of rows reads, for the split (a block is at most 256 rows)
-  const int at_once = L->G < 256 ? 256 / L->G : 1;
-  long long span = (long long)p.window + p.sinks + (n_q < at_once ? n_q : at_once) - 1;
-  if (span > c->n_tokens) span = c->n_tokens;
-  place_parts(&p, span, (char*)workspace + kHeader);
-  p.direct = p.splits == 1;
+  if ((st = check_end(what, workspace, ws_size, plan_window(L, &p, window, sinks, workspace))) != KVC_OK) return st;
   cudaGetLastError();
   cudaStream_t s = (cudaStream_t)stream;
-  st = launched(kvc::launch_dense_attn(p, s), "window attention launch");
-  if (st != KVC_OK || p.direct) return st;
-  return launched(kvc::launch_dense_combine(p, nullptr, s), "window attention merge launch");
+  st = launched(kvc::launch_dense_attn(p, s, false), "window attention launch");
+  if (st != KVC_OK || p.finish) return st;
+  return launched(kvc::launch_dense_combine(p, s), "window attention merge launch");
 }
 
 extern "C" size_t kvc_accum_workspace_bytes(const kvc_layout* L, int32_t n_tokens) {
   if (!L || L->d.kind != KVC_DENSE_BF16) return 0;
   const long long units = (long long)L->d.batch * L->d.n_kv_heads;
   if (too_large(units * L->L, L->G)) return 0;
-  return kHeader + part_bytes(L, units, L->G, n_tokens, false, false) + round_up((size_t)L->L * L->d.batch * L->d.n_q_heads * (size_t)(n_tokens > 0 ? n_tokens : 0) * 4, 256);
+  return kHeader + part_bytes(L, units, L->G, 1, n_tokens, false, false) +
+         round_up((size_t)L->L * L->d.batch * L->d.n_q_heads * (size_t)(n_tokens > 0 ? n_tokens : 0) * 4, 256);
 }
 
 extern "C" kvc_status kvc_decode_accum(const kvc_layout* L, const kvc_cache* c, const void* q, float* weights,
@@ -160,24 +211,21 @@ extern "C" kvc_status kvc_decode_accum(const kvc_layout* L, const kvc_cache* c, 
   if ((st = check_ws(what, workspace, ws_size, kvc_accum_workspace_bytes(L, c->n_tokens))) != KVC_OK) return st;
   p.q = (const __nv_bfloat16*)q;
   p.out = out;
-  p.err = (uint32_t*)workspace;
-  char* at = (char*)workspace + kHeader;
-  p.scores = (float*)at;
-  at += round_up((size_t)p.units * p.rows * (size_t)c->n_tokens * 4, 256);
-  place_parts(&p, c->n_tokens, at);
+  p.weights = weights;
+  if ((st = check_end(what, workspace, ws_size, plan_accum(&p, workspace))) != KVC_OK) return st;
   cudaGetLastError();
   cudaStream_t s = (cudaStream_t)stream;
-  st = launched(kvc::launch_dense_attn(p, s), "weighted decode launch");
-  if (st != KVC_OK) return st;
-  return launched(kvc::launch_dense_accum(p, weights, s), "weight sum launch");
+  st = launched(kvc::launch_dense_attn(p, s, false), "weighted decode launch");
+  if (st != KVC_OK || p.finish) return st;
+  return launched(kvc::launch_dense_accum(p, s), "weight sum launch");
 }
 
 extern "C" size_t kvc_prefix_workspace_bytes(const kvc_layout* L, int32_t n_tokens, int32_t n_prefix) {
   if (!L || L->d.kind != KVC_DENSE_BF16) return 0;
   const long long units = (long long)L->d.batch * L->d.n_kv_heads;
   if (too_large(units * L->L, L->G) || too_large((long long)L->L * L->d.n_kv_heads, (long long)L->d.batch * L->G)) return 0;
-  return kHeader + part_bytes(L, units, L->G, n_tokens, L->d.out_bf16, false) +
-         part_bytes(L, L->d.n_kv_heads, (long long)L->d.batch * L->G, n_prefix, L->d.out_bf16, false);
+  return kHeader + part_bytes(L, units, L->G, 1, n_tokens, L->d.out_bf16, false) +
+         part_bytes(L, L->d.n_kv_heads, (long long)L->d.batch * L->G, 1, n_prefix, L->d.out_bf16, false);
 }
 
 extern "C" kvc_status kvc_prefix_decode(const kvc_layout* PL, const kvc_cache* pc, const kvc_layout* L,
@@ -198,25 +246,14 @@ extern "C" kvc_status kvc_prefix_decode(const kvc_layout* PL, const kvc_cache* p
     return st;
   p.q = pre.q = (const __nv_bfloat16*)q;
   p.out = pre.out = out;
-  p.err = pre.err = (uint32_t*)workspace;
-  // the prefix's rows: every query head of the KV head's group, of every batch row
-  pre.out_bf16 = p.out_bf16;
-  pre.rows = L->d.batch * L->G;
-  pre.r_div = L->G;
-  pre.q_hi = p.q_row;
-  pre.q_row = p.q_row * L->d.batch;
-  pre.q_head = p.q_head;
-  char* at = (char*)workspace + kHeader;
-  place_parts(&p, c->n_tokens, at);
-  at += part_bytes(L, (long long)L->d.batch * p.Hkv, p.rows, c->n_tokens, p.out_bf16, false);
-  place_parts(&pre, pc->n_tokens, at);
+  if ((st = check_end(what, workspace, ws_size, plan_prefix(L, &p, &pre, workspace))) != KVC_OK) return st;
   cudaGetLastError();
   cudaStream_t s = (cudaStream_t)stream;
-  st = launched(kvc::launch_dense_attn(pre, s), "prefix attention launch");
+  st = launched(kvc::launch_dense_attn(pre, s, false), "prefix attention launch");
   if (st != KVC_OK) return st;
-  st = launched(kvc::launch_dense_attn(p, s), "own tokens' attention launch");
-  if (st != KVC_OK) return st;
-  return launched(kvc::launch_dense_combine(p, &pre, s), "prefix merge launch");
+  st = launched(kvc::launch_dense_attn(p, s, p.finish), "own tokens' attention launch");
+  if (st != KVC_OK || p.finish) return st;
+  return launched(kvc::launch_dense_combine(p, s), "prefix merge launch");
 }
 
 extern "C" kvc_status kvc_evict(const kvc_layout* SL, const kvc_cache* src, const kvc_layout* DL,
@@ -283,4 +320,24 @@ extern "C" kvc_status kvc_evict(const kvc_layout* SL, const kvc_cache* src, cons
   e.new_lens = new_lens;
   cudaGetLastError();
   return launched(kvc::launch_evict(e, (cudaStream_t)stream), "evict launch");
+}
+
+extern "C" int64_t kvc_test_dense_plan_bytes(const kvc_layout* L, int32_t op, int32_t n_tokens, int32_t n_2,
+                                             int32_t window, int32_t sinks, int32_t layer) {
+  kvc_cache c;
+  memset(&c, 0, sizeof(c));
+  char* const ws = (char*)4096;
+  c.k_dense = c.v_dense = ws;
+  c.n_tokens = n_tokens;
+  c.layer = layer;
+  kvc::DenseAttn p, pre;
+  if (!L || dense_problem("plan", L, &c, op == 0 ? n_2 : 1, &p) != KVC_OK) return -1;
+  if (op == 0) return plan_window(L, &p, window, sinks, ws) - ws;
+  if (op == 1) return plan_accum(&p, ws) - ws;
+  kvc_layout one = *L;
+  one.d.batch = 1;
+  one.d.max_tokens = n_2 > 0 ? n_2 : 1;
+  c.n_tokens = n_2;
+  if (dense_problem("plan", &one, &c, 1, &pre) != KVC_OK) return -1;
+  return plan_prefix(L, &p, &pre, ws) - ws;
 }

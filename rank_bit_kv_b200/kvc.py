@@ -194,6 +194,12 @@ class Layout:
         check(lib().kvc_create_layout(C.byref(desc), C.byref(h)))
         self.h = h
         self.desc = desc
+        self._sizes = None
+        # (layers, batch, query heads, KV heads, head dim, max_tokens, bf16 output) of a dense layout
+        self._dense = None
+        if desc.kind == KVC_DENSE_BF16:
+            self._dense = (max(1, desc.n_layers), desc.batch, desc.n_q_heads, desc.n_kv_heads, desc.head_dim,
+                           desc.max_tokens, bool(desc.out_bf16))
 
     def __del__(self):
         if getattr(self, "h", None) and _lib is not None:
@@ -207,7 +213,7 @@ class Layout:
 
     def buffer_sizes_cached(self):
         """buffer_sizes(), asked once (a layout is immutable)."""
-        if getattr(self, "_sizes", None) is None:
+        if self._sizes is None:
             self._sizes = self.buffer_sizes()
         return self._sizes
 
@@ -520,46 +526,60 @@ def _need(ok, what):
 
 def _tensor(t, name, dtype, shape, device):
     """t's address, after the checks that the C ABI cannot make."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _on(device, stream, call):
-    """call(stream) with `device` current; raises what the library reports."""
+def _run(device, stream, call, *args):
+    """call(*args, stream) with `device` current; raises what the library reports."""
     import torch
 
-    _need(device.type == "cuda", f"the tensors are on {device}, not on a GPU")
-    if device.index != torch.cuda.current_device():
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}, not on a GPU")
+    if device.index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
-            return _on(device, stream, call)
-    check(call(torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream))
+            return _run(device, stream, call, *args)
+    status = call(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream)
+    if status:
+        check(status)
 
 
 def _dense_dims(layout, cache):
-    """(leading layer axis, batch, query heads, KV heads, head dim) of a dense call."""
-    d = layout.desc
-    _need(d.kind == KVC_DENSE_BF16, "the serving operators take dense layouts")
-    lead = (d.n_layers,) if d.n_layers > 1 and not cache.layer else ()
-    return lead, d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim
+    """(leading layer axis, batch, query heads, KV heads, head dim, capacity, output type) of a dense call."""
+    import torch
+
+    if layout._dense is None:
+        raise ValueError("the serving operators take dense layouts")
+    layers, B, Hq, Hkv, d, cap, bf16 = layout._dense
+    return ((layers,) if layers > 1 and not cache.layer else (), B, Hq, Hkv, d, cap,
+            torch.bfloat16 if bf16 else torch.float32)
 
 
-def _check_cache(cache, device, batch):
+def _dense_cache(cache, device, batch):
+    """The cache's C struct, after checks of its buffers."""
     import torch
 
     sizes = cache.layout.buffer_sizes_cached()
-    for name in ("k_dense", "v_dense"):
-        t = cache.bufs[name]
-        _need(t.device == device and t.numel() * t.element_size() >= sizes[name] and t.is_contiguous(),
-              f"cache.{name} must be a contiguous buffer of {sizes[name]} bytes on {device}")
+    k, v = cache.bufs["k_dense"], cache.bufs["v_dense"]
+    for name, t in (("k_dense", k), ("v_dense", v)):
+        if t.device != device or t.nbytes < sizes[name] or not t.is_contiguous():
+            raise ValueError(f"cache.{name} must be a contiguous buffer of {sizes[name]} bytes on {device}")
+    c = CacheDesc()
+    c.k_dense = k.data_ptr()
+    c.v_dense = v.data_ptr()
+    c.n_tokens = cache.n_tokens
+    c.layer = cache.layer
     if cache.seq_lens is not None:
-        _tensor(cache.seq_lens, "cache.seq_lens", torch.int32, (batch,), device)
+        c.seq_lens = _tensor(cache.seq_lens, "cache.seq_lens", torch.int32, (batch,), device)
+    return c
 
 
-def _check_ws(ws, device):
-    _need(ws.device == device and ws.is_contiguous(), f"ws must be a contiguous buffer on {device}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+def _workspace(ws, device):
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous buffer on {device}")
+    return ws.data_ptr(), ws.nbytes
 
 
 def window_attn(layout: Layout, cache: Cache, q, out, ws, window, sinks=0, stream=None):
@@ -569,17 +589,15 @@ def window_attn(layout: Layout, cache: Cache, q, out, ws, window, sinks=0, strea
     ws at least layout.window_workspace_bytes(cache.n_tokens, n_q) bytes."""
     import torch
 
-    lead, B, Hq, _, d = _dense_dims(layout, cache)
+    lead, B, Hq, _, d, _, out_type = _dense_dims(layout, cache)
     dev = q.device
     _need(q.dim() == 4 + len(lead), "q must be [B, Hq, n_q, d] (all layers at once: [n_layers, B, Hq, n_q, d])")
     n_q = q.shape[-2]
     shape = (*lead, B, Hq, n_q, d)
     qp = _tensor(q, "q", torch.bfloat16, shape, dev)
-    op = _tensor(out, "out", torch.bfloat16 if layout.desc.out_bf16 else torch.float32, shape, dev)
-    _check_cache(cache, dev, B)
-    wp, wn = _check_ws(ws, dev)
-    cs = cache.struct()
-    _on(dev, stream, lambda st: lib().kvc_window_attn(layout.h, cs, qp, n_q, window, sinks, op, wp, wn, st))
+    op = _tensor(out, "out", out_type, shape, dev)
+    c = _dense_cache(cache, dev, B)
+    _run(dev, stream, lib().kvc_window_attn, layout.h, c, qp, n_q, window, sinks, op, *_workspace(ws, dev))
 
 
 def decode_accum(layout: Layout, cache: Cache, q, weights, out, ws, stream=None):
@@ -588,15 +606,13 @@ def decode_accum(layout: Layout, cache: Cache, q, weights, out, ws, stream=None)
     bf16 of that shape; ws at least layout.accum_workspace_bytes(cache.n_tokens)."""
     import torch
 
-    lead, B, Hq, Hkv, d = _dense_dims(layout, cache)
+    lead, B, Hq, Hkv, d, cap, out_type = _dense_dims(layout, cache)
     dev, shape = q.device, (*lead, B, Hq, d)
     qp = _tensor(q, "q", torch.bfloat16, shape, dev)
-    op = _tensor(out, "out", torch.bfloat16 if layout.desc.out_bf16 else torch.float32, shape, dev)
-    ap = _tensor(weights, "weights", torch.float32, (*lead, B, Hkv, layout.desc.max_tokens), dev)
-    _check_cache(cache, dev, B)
-    wp, wn = _check_ws(ws, dev)
-    cs = cache.struct()
-    _on(dev, stream, lambda st: lib().kvc_decode_accum(layout.h, cs, qp, ap, op, wp, wn, st))
+    op = _tensor(out, "out", out_type, shape, dev)
+    ap = _tensor(weights, "weights", torch.float32, (*lead, B, Hkv, cap), dev)
+    c = _dense_cache(cache, dev, B)
+    _run(dev, stream, lib().kvc_decode_accum, layout.h, c, qp, ap, op, *_workspace(ws, dev))
 
 
 def evict(src_layout: Layout, src_cache: Cache, dst_layout: Layout, dst_cache: Cache, weights, dst_weights,
@@ -608,18 +624,17 @@ def evict(src_layout: Layout, src_cache: Cache, dst_layout: Layout, dst_cache: C
     n_tokens and seq_lens (new_lens) afterwards."""
     import torch
 
-    lead, B, _, Hkv, _ = _dense_dims(src_layout, src_cache)
-    lead2, B2, _, Hkv2, _ = _dense_dims(dst_layout, dst_cache)
+    lead, B, _, Hkv, _, cap, _ = _dense_dims(src_layout, src_cache)
+    lead2, B2, _, Hkv2, _, cap2, _ = _dense_dims(dst_layout, dst_cache)
     dev = weights.device
-    ap = _tensor(weights, "weights", torch.float32, (*lead, B, Hkv, src_layout.desc.max_tokens), dev)
-    bp = _tensor(dst_weights, "dst_weights", torch.float32, (*lead2, B2, Hkv2, dst_layout.desc.max_tokens), dev)
-    _check_cache(src_cache, dev, B)
-    _check_cache(dst_cache, dev, B2)
+    ap = _tensor(weights, "weights", torch.float32, (*lead, B, Hkv, cap), dev)
+    bp = _tensor(dst_weights, "dst_weights", torch.float32, (*lead2, B2, Hkv2, cap2), dev)
+    a = _dense_cache(src_cache, dev, B)
+    b = _dense_cache(dst_cache, dev, B2)
     kept = torch.empty((*lead, B, Hkv, max(0, int(keep))), dtype=torch.int32, device=dev)
     lens = torch.empty((B,), dtype=torch.int32, device=dev)
-    a, b = src_cache.struct(), dst_cache.struct()
-    _on(dev, stream, lambda st: lib().kvc_evict(src_layout.h, a, dst_layout.h, b, ap, bp, keep, sinks, recent,
-                                                kept.data_ptr() or None, lens.data_ptr(), st))
+    _run(dev, stream, lib().kvc_evict, src_layout.h, a, dst_layout.h, b, ap, bp, keep, sinks, recent,
+         kept.data_ptr() or None, lens.data_ptr())
     return kept, lens
 
 
@@ -631,13 +646,11 @@ def prefix_decode(prefix_layout: Layout, prefix_cache: Cache, layout: Layout, ca
     layout.prefix_workspace_bytes(cache.n_tokens, prefix_cache.n_tokens) bytes."""
     import torch
 
-    lead, B, Hq, _, d = _dense_dims(layout, cache)
+    lead, B, Hq, _, d, _, out_type = _dense_dims(layout, cache)
     _dense_dims(prefix_layout, prefix_cache)
     dev, shape = q.device, (*lead, B, Hq, d)
     qp = _tensor(q, "q", torch.bfloat16, shape, dev)
-    op = _tensor(out, "out", torch.bfloat16 if layout.desc.out_bf16 else torch.float32, shape, dev)
-    _check_cache(prefix_cache, dev, 1)
-    _check_cache(cache, dev, B)
-    wp, wn = _check_ws(ws, dev)
-    a, b = prefix_cache.struct(), cache.struct()
-    _on(dev, stream, lambda st: lib().kvc_prefix_decode(prefix_layout.h, a, layout.h, b, qp, op, wp, wn, st))
+    op = _tensor(out, "out", out_type, shape, dev)
+    a = _dense_cache(prefix_cache, dev, 1)
+    b = _dense_cache(cache, dev, B)
+    _run(dev, stream, lib().kvc_prefix_decode, prefix_layout.h, a, layout.h, b, qp, op, *_workspace(ws, dev))

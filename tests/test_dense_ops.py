@@ -208,6 +208,25 @@ def test_workspace_grows_with_the_call():
         assert sizes == sorted(sizes) and sizes[0] >= 256
 
 
+def test_plans_stay_within_the_workspace():
+    """What a call's plan uses ends inside the bytes that the size query asks for."""
+    L = kvc.lib()
+    fn = L.kvc_test_dense_plan_bytes
+    fn.restype, fn.argtypes = C.c_int64, [C.c_void_p] + [C.c_int32] * 6
+    rng = np.random.default_rng(5)
+    for _ in range(3000):
+        B, Hkv, G, T = (int(2 ** rng.uniform(0, x)) for x in (8, 4, 6.5, 17))
+        lay = dense(B, G * Hkv, Hkv, int(rng.choice([64, 128])), T, int(rng.integers(1, 4)), int(rng.integers(0, 2)))
+        n, n_q = int(rng.integers(0, T + 1)), int(min(T, 2 ** rng.uniform(0, 12)))
+        W, S, layer = int(2 ** rng.uniform(0, 17)), int(rng.integers(0, 70)), int(rng.integers(0, 2))
+        need = (lay.window_workspace_bytes(n, n_q), lay.accum_workspace_bytes(n), lay.prefix_workspace_bytes(n, n_q))
+        for op, have in enumerate(need):
+            used = fn(lay.h, op, n, n_q, W, S, layer)
+            assert have == 0 or 0 <= used <= have, (B, Hkv, G, T, n, n_q, W, S, layer, op, used, have)
+        # a workspace sized for longer contexts and more query tokens serves shorter ones
+        assert need[0] == 0 or lay.window_workspace_bytes(n // 2, max(1, n_q // 3)) <= need[0]
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_shapes():
     import torch
 
@@ -778,3 +797,86 @@ def test_offsets_past_32_bits():
         ws = torch.empty(big.window_workspace_bytes(3000, n_q), dtype=torch.uint8, device="cuda")
         kvc.window_attn(big, cache, q, out, ws, 1000, 4)
         assert (out[1, 8] - o1[0, 0]).abs().max() < 1e-5
+
+
+def _on_gpu(q, k, v, seen, scale, bf16):
+    """(out, bound) of one head in 64 bits: q [r, d], k, v [t, d], seen [r, t]."""
+    import torch
+
+    q, k, v = q.double(), k.double(), v.double()
+    s = (q @ k.T * scale).masked_fill(~seen, -float("inf"))
+    p = torch.nan_to_num(torch.softmax(s, -1))
+    out, absv = p @ v, p @ v.abs()
+    size = float((q.abs() @ k.abs().T).max() * scale) if len(k) else 0.0
+    return _f64(out), D.error_bound(size, _f64(absv), _f64(out), q.shape[-1], bool(bf16), _p_bits(bf16)), p.sum(0)
+
+
+FLAT_LENS = [[4000, 1, 0, 3999, 2500, 16, 0, 3000], None, [0] * 7 + [4000], [4000] + [0] * 7]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", FLAT_LENS, ids=["ragged", "full", "last", "first"])
+@pytest.mark.parametrize("n_q,bf16,d,W,S", [(1, 0, 128, 4000, 0), (1, 1, 64, 3900, 70), (5, 0, 64, 3500, 3),
+                                            (3, 1, 128, 4000, 0)])
+def test_window_large_calls(lens, n_q, bf16, d, W, S):
+    """Enough tokens for every warp of the GPU: tiles dealt out across rows and heads."""
+    import torch
+
+    p = Problem(8, 12, 4, d, 4000, lens, cap=4011, bf16=bf16, seed=50)
+    q, out = p.queries(n_q, gain=1.5)
+    p.window(q, out, W, S)
+    for b, n in enumerate(p.lens):
+        pos = torch.arange(n - n_q, n, device="cuda")[:, None]
+        t = torch.arange(n, device="cuda")
+        for h in range(12):
+            ref, tol, _ = _on_gpu(q[b, h], p.k[b, h // 3, :n], p.v[b, h // 3, :n],
+                                  (t <= pos) & ((t < S) | (t > pos - W)), p.scale, bf16)
+            within(_f64(out[b, h]), ref, tol, f"row {b} head {h}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", FLAT_LENS[:2], ids=["ragged", "full"])
+@pytest.mark.parametrize("Hq,bf16,d", [(12, 0, 128), (16, 1, 128), (4, 0, 64), (132, 0, 64)])
+def test_accum_large_calls(lens, Hq, bf16, d):
+    import torch
+
+    p = Problem(8, Hq, 4, d, 4000, lens, cap=4011, bf16=bf16, seed=51)
+    q, out = p.queries(gain=1.5)
+    w = torch.rand(8, 4, 4011, generator=p.gen, device="cuda")
+    w0 = w.double()
+    kvc.decode_accum(p.layout, p.cache, q, w, out, p.ws(p.layout.accum_workspace_bytes(4000)))
+    G = Hq // 4
+    for b, n in enumerate(p.lens):
+        every = torch.ones(G, n, dtype=torch.bool, device="cuda")
+        for h in range(4):
+            k = p.k[b, h, :n]
+            ref, tol, dw = _on_gpu(q[b, h * G:(h + 1) * G], k, p.v[b, h, :n], every, p.scale, bf16)
+            within(_f64(out[b, h * G:(h + 1) * G]), ref, tol, f"row {b} head {h}")
+            size = float((q[b, h * G:(h + 1) * G].double().abs() @ k.double().abs().T).max() * p.scale) if n else 0.0
+            want = w0[b, h, :n] + dw
+            rel = 2 * (d / 16) * 2.0**-22 * size + 2.0**-19
+            assert ((w[b, h, :n].double() - want).abs() <= rel * dw + 2.0**-24 * want).all()
+        assert torch.equal(w[b, :, n:].double(), w0[b, :, n:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bf16", [0, 1])
+@pytest.mark.parametrize("B,T,P", [(64, 600, 4000), (64, 0, 4000), (64, 600, 0), (3, 9, 40000)])
+def test_prefix_large_calls(bf16, B, T, P):
+    import torch
+
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, T + 1, B)]
+    p = Problem(B, 16, 4, 128, max(T, 1), lens, cap=T + 7, bf16=bf16, seed=52)
+    p.cache.n_tokens = T
+    pre = Problem(1, 16, 4, 128, max(P, 1), cap=P + 3, seed=53)
+    pre.cache.n_tokens = P
+    q, out = p.queries(gain=1.5)
+    kvc.prefix_decode(pre.layout, pre.cache, p.layout, p.cache, q, out, p.ws(p.layout.prefix_workspace_bytes(T, P)))
+    for b in range(0, B, 5):
+        for h in range(4):
+            k = torch.cat([pre.k[0, h, :P], p.k[b, h, :lens[b]]])
+            v = torch.cat([pre.v[0, h, :P], p.v[b, h, :lens[b]]])
+            ref, tol, _ = _on_gpu(q[b, 4 * h:4 * h + 4], k, v,
+                                  torch.ones(4, len(k), dtype=torch.bool, device="cuda"), p.scale, bf16)
+            within(_f64(out[b, 4 * h:4 * h + 4]), ref, tol, f"row {b} head {h}")
