@@ -9,11 +9,12 @@
 // at d = 128) and 128^2 exponentials (1024 clocks at 16 a clock).  So two score
 // tiles ("streams") are in flight per CTA, and while the softmax of one runs on
 // its four warps the tensor core works on the other:
-//   warps 0-3, 4-7  softmax of stream 0 / 1, one thread per row: scores from TMEM,
-//                   mask, maximum, exponentials, P back into TMEM over the scores
-//   warp 8          issues the MMAs: S = Q K^T from shared memory, O += P V with P
-//                   from TMEM
-//   warp 9          loads 128-token tiles of K and V by TMA into a ring
+//   warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row: scores from TMEM,
+//                    mask, maximum, exponentials, P back into TMEM over the scores
+//   warp 8           issues the MMAs: S = Q K^T from shared memory, O += P V with P
+//                    from TMEM (one warp per stream: 427 us for the prefill of 8192
+//                    tokens that took 335 so; interleaved MMAs of two warps run slower)
+//   warp 9           loads 128-token tiles of K and V by TMA into a ring
 // PAIR: the streams are two tiles of 128 query rows and share the K/V tiles.
 // Otherwise (up to 128 rows, or too few blocks to fill the SMs) they are the
 // same 128 rows over the even and the odd tiles, merged through shared memory.
@@ -36,6 +37,7 @@ constexpr int kTN = 128;                 // tokens per tile
 constexpr int kWarpMma = 8, kWarpTma = 9;
 constexpr int kThreads = 320;
 constexpr int kSoftThreads = 256;
+constexpr float kSlack = 24.f;           // how far scores may pass the reference maximum (log2)
 
 template <int D>
 struct Cfg {
@@ -69,6 +71,44 @@ __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// 1 in one lane of the warp.  The MMAs and commits are executed by the whole warp and
+// predicated on it: in uniform control flow the descriptors live in uniform registers,
+// where the instruction takes them.  Eight MMAs take about 300 clocks to issue so, 700
+// under a branch or a predicate on the lane number, and 512 to execute.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t lead;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(lead));
+  return lead;
+}
+__device__ __forceinline__ void mma_ss_lead(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_lead(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_lead(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -96,6 +136,16 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
   return d;
 }
+// NaN where any of them is.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Bits 0 .. i (none below 0, all from 31).
+__device__ __forceinline__ uint32_t bits_to(int i) {
+  return i < 0 ? 0u : 0xffffffffu >> (31 - min(i, 31));
+}
 __device__ __forceinline__ uint32_t pack_bf2(float2 x) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -104,7 +154,7 @@ __device__ __forceinline__ uint32_t pack_bf2(float2 x) {
 template <int D>
 struct __align__(8) Bars {
   uint64_t q_full, full[Cfg<D>::kStages], empty[Cfg<D>::kStages];
-  uint64_t s_full[2], p_full[2], o_done[2], drain;
+  uint64_t s_full[2], p_full[2][2], o_done[2], drain;       // p_full: [stream][half of the tokens]
   uint32_t tmem;
   int abort;
   float ml[kTM][2];                      // stream 1's maximum and sum
@@ -165,11 +215,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.clear_err && blockIdx.x == 0 && threadIdx.x == 0) *err = 0u;
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars.q_full, kSoftThreads);
+    mbar_init(&bars.q_full, kSoftThreads / 32);
     for (int i = 0; i < NST; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.s_full[s], 1);
-      mbar_init(&bars.p_full[s], kTM);
+      mbar_init(&bars.p_full[s][0], kTM / 32);
+      mbar_init(&bars.p_full[s][1], kTM / 32);
       mbar_init(&bars.o_done[s], 1);
     }
     mbar_init(&bars.drain, 1);
@@ -219,44 +270,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kWarpMma) {
-    // ---- MMAs
+    // ---- MMAs.  What the descriptors derive from is broadcast, so that the compiler
+    // knows it as uniform.
+    auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const int n = uniform(tl.n);
+    const uint32_t tmem = (uint32_t)uniform((int)bars.tmem);
+    Tiles tu;
+    tu.sp.a1 = uniform(tl.sp.a1);
+    tu.sp.b0 = uniform(tl.sp.b0);
+    tu.sp.b1 = uniform(tl.sp.b1);
+    tu.n_a = uniform(tl.n_a);
+    tu.first = uniform(tl.first);
+    tu.n = n;
     if (n > 0) {
       bool ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full, 0, abort, err));
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
-      };
-      auto qk = [&](int s, int t, bool first_use, bool last_use) {
-        const int pos = ring_k<PAIR>(t), st = pos % NST;
-        if (first_use) wait(&bars.full[st], (pos / NST) & 1);
-        if (!ok) return;
         tc_fence_after();
-        if (lane == 0) {
-          int t0, nt;
-          tl.at(t, t0, nt);
-          const uint32_t id = idesc_bf16((nt + 15) & ~15, 0);
-          const uint32_t qa = smem_u32(sm_q + (PAIR ? s * C::kTileB : 0));
-          const uint32_t ka = smem_u32(ring + st * C::kTileB);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * C::kHalfB + (kk % 4) * 32;
-            mma_ss(tmem + col_s(s), desc_sw128(qa + off, 0, 1024), desc_sw128(ka + off, 0, 1024), id, kk > 0);
-          }
-          tc_commit(&bars.s_full[s]);
-          if (last_use) tc_commit(&bars.empty[st]);
-        }
-        __syncwarp();
       };
-      auto pv = [&](int s, int j, int t, bool first_use, bool last_use) {
-        const int pos = ring_v<PAIR>(t, n), st = pos % NST;
+      const uint32_t lead = elect_one();
+      const uint32_t ring0 = smem_u32(ring), qa = smem_u32(sm_q);
+      // S of stream s over K tile t
+      auto qk = [&](int s, int t) {
         int t0, nt;
-        tl.at(t, t0, nt);
+        tu.at(t, t0, nt);
+        const uint32_t id = idesc_bf16((nt + 15) & ~15, 0), sd = tmem + col_s(s);
+        const uint64_t qd = desc_sw128(qa + (PAIR ? s * C::kTileB : 0), 0, 1024);
+        const uint64_t kd = desc_sw128(ring0 + ring_k<PAIR>(t) % NST * C::kTileB, 0, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk / 4) * C::kHalfB + (kk % 4) * 32) >> 4;
+          mma_ss_lead(lead, sd, qd + off, kd + off, id, kk > 0);
+        }
+      };
+      auto full = [&](int pos) { wait(&bars.full[pos % NST], (pos / NST) & 1); };
+      auto release = [&](int pos) { commit_lead(lead, &bars.empty[pos % NST]); };
+      constexpr int hop = PAIR ? 1 : 2;                  // a stream's tiles are t, t + hop, ...
+      // stream s: O over V tile t (its j-th), and S over the next K tile, issued in one
+      // go; first, last: it is the first or last stream to use these tiles
+      auto step = [&](int s, int j, int t, bool first, bool last) {
+        const int pos_v = ring_v<PAIR>(t, n), pos_k = ring_k<PAIR>(t + hop);
+        const bool next = t + hop < n;
+        int t0, nt;
+        tu.at(t, t0, nt);
         const int steps = (nt + 15) / 16;
-        uint8_t* const vt = ring + st * C::kTileB;
-        if (first_use) {
-          wait(&bars.full[st], (pos / NST) & 1);
-          if (!ok) return;
-          if (nt & 15) {
+        if (first) {
+          full(pos_v);
+          if (ok && (nt & 15)) {
             // rows behind the range, in its last 16: zero, whatever the cache holds there
+            uint8_t* const vt = ring + pos_v % NST * C::kTileB;
             const int i0 = nt * 8, i1 = steps * 16 * 8;
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
@@ -265,36 +327,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
+          if (next) full(pos_k);
         }
-        wait(&bars.p_full[s], j & 1);
-        if (!ok) return;
-        tc_fence_after();
-        if (lane == 0) {
-          constexpr uint32_t id = idesc_bf16(D, 1);
-          const uint32_t va = smem_u32(vt);
-          for (int ks = 0; ks < steps; ++ks)
-            mma_ts(tmem + col_o<D>(s), tmem + col_s(s) + 8 * ks, desc_sw128(va + ks * 2048, C::kHalfB, 1024), id,
-                   j > 0 || ks > 0);
-          tc_commit(&bars.o_done[s]);
-          if (last_use) tc_commit(&bars.empty[st]);
+        constexpr uint32_t id = idesc_bf16(D, 1);
+        const uint64_t vd = desc_sw128(ring0 + pos_v % NST * C::kTileB, C::kHalfB, 1024);
+        const uint32_t sd = tmem + col_s(s), od = tmem + col_o<D>(s);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          wait(&bars.p_full[s][h], j & 1);
+          if (!ok) return;
+          if (steps == kTN / 16) {
+#pragma unroll
+            for (int k = 0; k < kTN / 32; ++k) {
+              const int ks = h * (kTN / 32) + k;
+              mma_ts_lead(lead, od, sd + 8 * ks, vd + ks * 128, id, j > 0 || ks > 0);
+            }
+          } else {
+            for (int ks = h * (kTN / 32); ks < min(steps, (h + 1) * (kTN / 32)); ++ks)
+              mma_ts_lead(lead, od, sd + 8 * ks, vd + ks * 128, id, j > 0 || ks > 0);
+          }
         }
-        __syncwarp();
+        if (next) {
+          qk(s, t + hop);
+          commit_lead(lead, &bars.s_full[s]);
+        }
+        commit_lead(lead, &bars.o_done[s]);
+        if (last) {
+          release(pos_v);
+          if (next) release(pos_k);
+        }
       };
-      if (PAIR) {
-        qk(0, 0, true, false);
-        qk(1, 0, false, true);
-        for (int t = 0; t < n && ok; ++t) {
-          pv(0, t, t, true, false);
-          if (t + 1 < n) qk(0, t + 1, true, false);
-          pv(1, t, t, false, true);
-          if (t + 1 < n) qk(1, t + 1, false, true);
+      full(ring_k<PAIR>(0));
+      if (ok) {
+        qk(0, 0);
+        commit_lead(lead, &bars.s_full[0]);
+        if (!PAIR) release(0);
+      }
+      if (PAIR || n > 1) {
+        if (!PAIR) full(ring_k<PAIR>(1));
+        if (ok) {
+          qk(1, PAIR ? 0 : 1);
+          commit_lead(lead, &bars.s_full[1]);
+          release(PAIR ? 0 : ring_k<PAIR>(1));
         }
-      } else {
-        qk(0, 0, true, true);
-        if (n > 1) qk(1, 1, true, true);
-        for (int t = 0; t < n && ok; ++t) {
-          pv(t & 1, t >> 1, t, true, true);
-          if (t + 2 < n) qk(t & 1, t + 2, true, true);
+      }
+      for (int t = 0; t < n && ok; ++t) {
+        if (PAIR) {
+          step(0, t, t, true, false);
+          step(1, t, t, false, true);
+        } else {
+          step(t & 1, t >> 1, t, true, true);
         }
       }
       if (!ok && lane == 0) {
@@ -310,18 +392,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;              // row of the stream = TMEM lane
     const uint32_t tl_base = tmem + ((uint32_t)(warp & 3) << 21);
     if (n > 0) {
-      // queries, 16 bytes a thread and step; zero past the block's rows
-      constexpr int CH = D / 8;                          // 16-byte chunks of a row
-      for (int i = threadIdx.x; i < RB * CH; i += kSoftThreads) {
-        const int r = i / CH, c = i % CH;
-        const bool has = r < n_rows;
-        const __nv_bfloat16* src = p.q + dense_row_at(p, u, r0 + (has ? r : 0)) + c * 8;
-        uint8_t* dst = sm_q + (r / kTM) * C::kTileB + (c / 8) * C::kHalfB + (r % kTM) * 128 + (((c & 7) ^ (r & 7)) << 4);
-        cp_async16(dst, src, has ? 16 : 0);
+      // queries: a warp its rows, neighbouring lanes the chunks of one (a row per lane
+      // takes 4000 clocks more of the copies' issue); zero past the block's rows
+      constexpr int RPW = RB / 8, CPR = D / 8, RPI = 32 / CPR;
+      const int mine = warp * RPW + lane % RPW;
+      const long long off = dense_row_at(p, u, r0 + min(mine, n_rows - 1));
+#pragma unroll
+      for (int i = 0; i < RPW / RPI; ++i) {
+        const int k = i * RPI + lane / CPR, r = warp * RPW + k, c = lane % CPR;
+        const __nv_bfloat16* src = p.q + __shfl_sync(0xffffffffu, off, k) + c * 8;
+        cp_async16(sm_q + (r / kTM) * C::kTileB + (c / 8) * C::kHalfB + (r % kTM) * 128 + (((c & 7) ^ (r & 7)) << 4), src,
+                   r < n_rows ? 16 : 0);
       }
       cp_async_wait_all();
       fence_proxy_async_smem();
-      mbar_arrive(&bars.q_full);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.q_full);
     }
     const int r = (PAIR ? s * kTM : 0) + row;            // row of the block
     const int pos = dense_row_pos(p, len, r0 + min(r, n_rows - 1));
@@ -338,63 +424,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[s], j & 1, abort, err)))) break;
       tc_fence_after();
       uint32_t x[4][32];
-      const int chunks = (nt + 31) >> 5;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (c < chunks) tmem_ld32(tl_base + col_s(s) + 32 * c, x[c]);
+        tmem_ld32(tl_base + col_s(s) + 32 * c, x[c]);
       tmem_wait_ld();
 #pragma unroll
       for (int c = 0; c < 4; ++c) reg_fence(x[c]);
       // a tile that every row sees whole needs no mask
-      if (nt < kTN || t0 + kTN - 1 > s_lo || !(t0 + kTN <= p.sinks || t0 > s_hi - p.window)) {
-        const int hi = min(pos - t0, nt - 1), lo = pos - p.window + 1 - t0, sk = p.sinks - t0;
+      const bool masked = nt < kTN || t0 + kTN - 1 > s_lo || !(t0 + kTN <= p.sinks || t0 > s_hi - p.window);
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int base = t0 + 32 * c;
+          // bit i: token base + i is seen
+          const uint32_t seen =
+              bits_to(min(pos, t0 + nt - 1) - base) & (~bits_to(pos - p.window - base) | bits_to(p.sinks - 1 - base));
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(seen >> i & 1u)) x[c][i] = 0xff800000u;
+        }
+      }
+      auto maximum = [&]() {
+        float m8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m8[k] = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int t = 32 * c + i;
-            if (!(t <= hi && (t >= lo || t < sk))) x[c][i] = 0xff800000u;
-          }
-      }
-      float mx = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < chunks) {
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[c][i]));
-          mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-        }
-      mx *= p.scale_log2;
-      // the reference maximum is raised only by a score more than 2^8 above it
-      if (__any_sync(0xffffffffu, mx > m_ref + 8.f)) {
-        const float nm = fmaxf(m_ref, mx);
-        const float a = nm == -INFINITY ? 1.f : ex2_approx(m_ref - nm);
-        m_ref = nm;
-        l *= a;
-        if (j > 0) {
-          // the last product is in the accumulators before they are rescaled
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_done[s], (j - 1) & 1, abort, err)))) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(tl_base + col_o<D>(s) + c, o);
-            tmem_wait_ld();
-            reg_fence(o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-            tmem_st16(tl_base + col_o<D>(s) + c, o);
-          }
-          tmem_wait_st();
-        }
-      }
-      const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-      const float2 neg2 = make_float2(neg, neg);
+          for (int i = 0; i < 32; i += 2)
+            m8[i / 2 & 7] = max3(m8[i / 2 & 7], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+        return max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), max3(m8[6], m8[7], m8[7])) * p.scale_log2;
+      };
+      // exponentials of two chunks: sums to `sum`, P to TMEM.  (A cubic on the FMA pipes
+      // for a quarter or half of them: 300 and 315 us where this takes 290: the issue of
+      // instructions is what a softmax warp lacks, not the special function unit.)
       float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+      auto exps = [&](int c0) {
+        const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+        const float2 neg2 = make_float2(neg, neg);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < chunks) {
+        for (int c = c0; c < c0 + 2; ++c) {
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -406,11 +475,58 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_st16(tl_base + col_s(s) + 16 * c, w);
         }
+      };
+      auto arrive = [&](int h) {                         // one arrival per warp: they are taken one by one
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[s][h]);
+      };
+      // The reference maximum is raised only by a score more than 2^kSlack above it (P, its
+      // sums and the products have room for that), so the exponentials start without the
+      // maximum, which the arithmetic pipes find beside them.
+      bool late = __any_sync(0xffffffffu, m_ref == -INFINITY) || masked;
+      if (!late) {
+        exps(0);
+        const float mx = maximum();
+        late = !__all_sync(0xffffffffu, mx <= m_ref + kSlack);         // NaN: the other path keeps it
+        if (!late) {
+          arrive(0);
+          exps(2);
+        } else {
+          sum[0] = sum[1] = make_float2(0.f, 0.f);
+        }
+      }
+      if (late) {
+        const float mx = maximum();
+        if (__any_sync(0xffffffffu, mx > m_ref + kSlack)) {
+          const float nm = fmaxf(m_ref, mx);
+          const float a = nm == -INFINITY ? 1.f : ex2_approx(m_ref - nm);
+          m_ref = nm;
+          l *= a;
+          if (j > 0) {
+            // the last product is in the accumulators before they are rescaled
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_done[s], (j - 1) & 1, abort, err)))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tl_base + col_o<D>(s) + c, o);
+              tmem_wait_ld();
+              reg_fence(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tmem_st16(tl_base + col_o<D>(s) + c, o);
+            }
+          }
+        }
+        exps(0);
+        arrive(0);
+        exps(2);
+      }
+      arrive(1);
       sum[0] = add2(sum[0], sum[1]);
       l += sum[0].x + sum[0].y;
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&bars.p_full[s]);
     }
     // ---- epilogue
     if (ok && n_s > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_done[s], (n_s - 1) & 1, abort, err));
@@ -436,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       named_bar(1, kSoftThreads);
     }
-    if (ok && (PAIR || s == 0) && r - (r & 31) < n_rows) {
+    if ((PAIR || s == 0) && r - (r & 31) < n_rows) {
       float a0 = 1.f, a1 = 0.f;
       // a stream that saw nothing adds nothing
       const bool mine = !(m_ref == -INFINITY && l == 0.f);
@@ -455,21 +571,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const size_t at = (size_t)blockIdx.x * RB + r;
       const long long out_at = dense_row_at(p, u, r0 + min(r, n_rows - 1));
-      bool fine = true;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
+      // rows go through shared memory (the stream's queries' place: their products are
+      // over), 2 D bytes of each of the warp's rows at a time, and out with neighbouring
+      // lanes on one row.  16-byte chunk c of row i is at chunk c ^ i.
+      constexpr int CPR = D / 8, RPI = 32 / CPR;             // chunks per row, rows per step of a warp
+      uint8_t* const rows = sm_q + warp * 32 * (2 * D);
+      auto chunk = [&](int i, int c) {
+        return reinterpret_cast<uint4*>(rows + i * (2 * D) + ((c ^ (i & (CPR - 1))) << 4));
+      };
+      auto values = [&](int c, float (&f)[16]) {
         uint32_t o[16];
         tmem_ld16(tl_base + col_o<D>(s) + c, o);
         tmem_wait_ld();
         reg_fence(o);
-        float f[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           f[i] = mine ? __uint_as_float(o[i]) * a0 : 0.f;
           if (other) f[i] = fmaf(a1, stage[(c + i) * kTM + row], f[i]);
           if (l == 0.f) f[i] = 0.f;
         }
-        if (p.finish) {
+      };
+      const int n_here = min(32, n_rows - (r - lane));       // rows of this warp
+      bool fine = true;
+      if (ok && p.finish) {
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          float f[16];
+          values(c, f);
           uint32_t w[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -477,33 +605,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             fine = fine && fabsf(v.x) <= 3.4e38f && fabsf(v.y) <= 3.4e38f;
             w[i] = pack_bf2(v);
           }
-          if (r < n_rows) {
-            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + out_at + c);
-            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-          }
-        } else if (r < n_rows) {
-          float4* dst = reinterpret_cast<float4*>(p.own.part + at * D + c);
+          *chunk(lane, c / 8) = make_uint4(w[0], w[1], w[2], w[3]);
+          *chunk(lane, c / 8 + 1) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int k = i * RPI + lane / CPR, c = lane % CPR;
+          const long long to = __shfl_sync(0xffffffffu, out_at, k);
+          if (k < n_here) reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + to)[c] = *chunk(k, c);
+        }
+      } else if (ok) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-        }
-      }
-      if (p.finish) {
-        // rows that another row's NaN or infinity may have reached: from the definition
-        if (p.n_q > 1) {
-          unsigned bad = __ballot_sync(0xffffffffu, !fine && r < n_rows);
-          __syncwarp();
-          while (bad) {
-            const int b = __ffs(bad) - 1;
-            bad &= bad - 1;
-            float o[D / 32];
-            const int rr = r0 + r - lane + b;
-            dense_row_alone<D>(p, u, rr, o);
-            dense_put_row<D>(p, u, rr, o);
+        for (int c0 = 0; c0 < D; c0 += D / 2) {
+#pragma unroll
+          for (int c = 0; c < D / 2; c += 16) {
+            float f[16];
+            values(c0 + c, f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *chunk(lane, c / 4 + i) = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                                                   __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
           }
+          __syncwarp();
+#pragma unroll 4
+          for (int i = 0; i < 32 / RPI; ++i) {
+            const int k = i * RPI + lane / CPR, c = lane % CPR;
+            if (k < n_here) reinterpret_cast<uint4*>(p.own.part + (at - lane + k) * D + c0)[c] = *chunk(k, c);
+          }
+          __syncwarp();
         }
-      } else if (r < n_rows) {
-        *reinterpret_cast<float2*>(p.own.ml + 2 * at) = make_float2(m_ref, l);
+        if (r < n_rows) *reinterpret_cast<float2*>(p.own.ml + 2 * at) = make_float2(m_ref, l);
+      }
+      if (p.finish && p.n_q > 1) {
+        // rows that another row's NaN or infinity may have reached: from the definition
+        unsigned bad = __ballot_sync(0xffffffffu, ok && !fine && r < n_rows);
+        __syncwarp();
+        while (bad) {
+          const int b = __ffs(bad) - 1;
+          bad &= bad - 1;
+          float o[D / 32];
+          const int rr = r0 + r - lane + b;
+          dense_row_alone<D>(p, u, rr, o);
+          dense_put_row<D>(p, u, rr, o);
+        }
       }
     }
   }
