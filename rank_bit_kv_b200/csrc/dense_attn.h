@@ -136,6 +136,7 @@ struct EvictCall {
   const int* seq_lens;
   int keep, sinks, recent;
   int in_place;
+  int blocks;                   // of the selection, per unit (set by the launch)
   int* kept;                    // [units, keep]
   int* new_lens;                // [B]
 };

@@ -4,13 +4,15 @@
 // `recent` are kept always; the rest of the `keep` places go to the largest
 // running sums, equal ones to the lower position.  Kept tokens stay in order.
 //
-//   select_kernel  one block per unit.  A radix select over the sums' 32-bit
-//                  patterns (monotone for sums >= 0) finds the smallest kept sum
-//                  and how many tokens equal to it are kept; then each warp
-//                  counts its stretch of positions, the counts are scanned, and
-//                  each warp writes its kept positions.  Reads the sums once.
-//   gather kernels copy the kept rows of K and V and the sums: bound by memory,
-//                  4 d bytes read and written per kept token.
+//   select_kernel  a cluster of up to 8 blocks per unit, a stretch of positions each,
+//                  the sums in shared memory.  A radix select over the sums' 32-bit
+//                  patterns (monotone for sums >= 0; histograms added up through
+//                  distributed shared memory) finds the smallest kept sum and how
+//                  many tokens equal to it are kept; then each warp counts its
+//                  stretch of positions, the counts are scanned, and each warp
+//                  writes its kept positions and sums.  Reads the sums once.
+//   gather, move   copy the kept rows of K and V: bound by memory, 4 d bytes read and
+//                  written per kept token.
 #include <math.h>
 
 #include "dense_attn.h"
@@ -22,7 +24,27 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;              // 11 bits a pass: 11 + 11 + 10
-constexpr int kStageTok = 48 * 1024;     // sums held in shared memory
+constexpr int kStageTok = 48 * 1024;     // sums held in a block's shared memory
+constexpr int kMaxBlocks = 8;            // blocks of a cluster
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint2 ld_rank(const void* p, int rank) {
+  uint32_t a;
+  uint2 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ unsigned scan_up(unsigned v) {      // inclusive sum over the lanes up to this one
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned x = __shfl_up_sync(0xffffffffu, v, o);
+    if ((int)(threadIdx.x & 31) >= o) v += x;
+  }
+  return v;
+}
 
 __device__ __forceinline__ int evict_len(const EvictCall& p, int u) {
   int n = p.n_tokens;
@@ -37,98 +59,132 @@ __device__ __forceinline__ uint32_t sum_key(float w) { return w > 0.f ? __float_
 
 template <bool STAGED>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictCall p) {
-  extern __shared__ uint32_t keys_sm[];  // STAGED: the candidates' keys
-  __shared__ unsigned hist[kBins];
+  extern __shared__ float sums[];        // STAGED: the block's stretch of the row's sums
+  __shared__ __align__(8) unsigned hist[2][kBins];
   __shared__ unsigned warp_a[kSelWarps], warp_b[kSelWarps];
   __shared__ unsigned sh_digit, sh_need;
-  const int u = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ uint2 total;                // this block's kept tokens, and those equal to the boundary
+  const int C = p.blocks, rank = blockIdx.x % C, u = blockIdx.x / C;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = evict_len(p, u);
   const int new_len = min(len, p.keep);
   int* const kept = p.kept + (size_t)u * p.keep;
-  if (u < p.B * p.Hkv && u % p.Hkv == 0 && tid == 0) p.new_lens[u / p.Hkv] = new_len;
-  for (int i = new_len + tid; i < p.keep; i += kSelThreads) kept[i] = -1;
-  if (len <= p.keep) {
-    for (int i = tid; i < len; i += kSelThreads) kept[i] = i;
-    return;
-  }
-  // candidates: tokens [c0, c1), of which `need` are kept (sinks + recent <= keep < len)
-  const int c0 = p.sinks, c1 = len - p.recent;
-  const int n_c = c1 - c0;
-  unsigned need = (unsigned)(p.keep - p.sinks - p.recent);
-  const float* w = p.w + (size_t)u * p.tmax + c0;
-  auto key_at = [&](int i) { return STAGED ? keys_sm[i] : sum_key(w[i]); };
-  if (STAGED) {
-    for (int i = tid; i < n_c; i += kSelThreads) keys_sm[i] = sum_key(w[i]);
-  }
-  // the key of the need-th largest candidate, digit by digit from the top;
-  // need becomes the number of candidates equal to it that are kept
-  uint32_t prefix = 0;
-  int shift = 32;
-  for (int pass = 0; pass < 3; ++pass) {
-    const int bits = pass == 2 ? 10 : 11;
-    const uint32_t hi = pass == 0 ? 0u : ~0u << shift;
-    shift -= bits;
-    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < n_c; i += kSelThreads) {
-      const uint32_t k = key_at(i);
-      if ((k & hi) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+  const float* const w = p.w + (size_t)u * p.tmax;
+  float* const w2 = p.w2 + (size_t)u * p.tmax2;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (u < p.B * p.Hkv && u % p.Hkv == 0 && rank == 0 && tid == 0) p.new_lens[u / p.Hkv] = new_len;
+  // this block's positions [q0, q1)
+  const int per_block = ((len + C - 1) / C + 31) & ~31;
+  const int q0 = min(len, rank * per_block), q1 = min(len, q0 + per_block);
+  if (STAGED)
+    for (int t = q0 + tid; t < q1; t += kSelThreads) sums[t - q0] = w[t];
+  auto sum_at = [&](int t) { return STAGED ? sums[t - q0] : w[t]; };
+  for (int i = new_len + rank * kSelThreads + tid; i < p.keep; i += C * kSelThreads) kept[i] = -1;
+  if (len <= p.keep) {                   // the row keeps all
+    if (STAGED) cluster_sync();          // in place: read before written
+    for (int t = q0 + tid; t < q1; t += kSelThreads) {
+      kept[t] = t;
+      if (STAGED) w2[t] = sums[t - q0];
     }
-    __syncthreads();
-    // suffix sums of the bins: thread t owns bins 2t, 2t + 1
-    const unsigned a = hist[2 * tid], b = hist[2 * tid + 1];
-    unsigned v = a + b;                  // sum over this lane and the lanes above it
+  } else {
+    // candidates: tokens [c0, c1), of which `need` are kept (sinks + recent <= keep < len)
+    const int c0 = p.sinks, c1 = len - p.recent;
+    const int h0 = max(q0, c0), h1 = min(q1, c1);
+    unsigned need = (unsigned)(p.keep - p.sinks - p.recent);
+    // the key of the need-th largest candidate, digit by digit from the top;
+    // need becomes the number of candidates equal to it that are kept
+    uint32_t prefix = 0;
+    int shift = 32;
+    for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int bits = pass == 2 ? 10 : 11;
+      const uint32_t hi = pass == 0 ? 0u : ~0u << shift;
+      unsigned* const mine = hist[pass & 1];
+      shift -= bits;
+      __syncthreads();
+      for (int t = h0 + tid; t < h1; t += kSelThreads) {
+        const uint32_t k = sum_key(sum_at(t));
+        if ((k & hi) == prefix) atomicAdd(&mine[(k >> shift) & ((1u << bits) - 1u)], 1u);
+      }
+      cluster_sync();
+      // the other histogram is not read any more: zero for the next pass
+      hist[(pass + 1) & 1][2 * tid] = hist[(pass + 1) & 1][2 * tid + 1] = 0;
+      // suffix sums of the cluster's bins: thread t owns bins 2t, 2t + 1
+      unsigned a = 0, b = 0;
+      for (int c = 0; c < C; ++c) {
+        const uint2 x = ld_rank(&mine[2 * tid], c);
+        a += x.x;
+        b += x.y;
+      }
+      unsigned v = a + b;                // sum over this lane and the lanes above it
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned x = __shfl_down_sync(0xffffffffu, v, o);
-      if (lane + o < 32) v += x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_down_sync(0xffffffffu, v, o);
+        if (lane + o < 32) v += x;
+      }
+      if (lane == 0) warp_a[warp] = v;
+      __syncthreads();
+      const unsigned above = __reduce_add_sync(0xffffffffu, lane > warp ? warp_a[lane] : 0u);
+      const unsigned over = above + v - (a + b);        // candidates in bins above 2 tid + 1
+      if (need > over && need <= over + b) sh_digit = 2 * tid + 1, sh_need = need - over;
+      else if (need > over + b && need <= over + b + a) sh_digit = 2 * tid, sh_need = need - over - b;
+      if (need == 0 && tid == 0) sh_digit = kBins - 1, sh_need = 0;
+      __syncthreads();
+      prefix |= (sh_digit & ((1u << bits) - 1u)) << shift;
+      need = sh_need;
     }
-    if (lane == 0) warp_a[warp] = v;
+    // need == 0 (nothing but the protected tokens): the key is above every sum
+    if (p.keep == p.sinks + p.recent) prefix = 0xffffffffu;
+    // each warp takes a stretch of the block's positions
+    const int per = (q1 - q0 + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
+    const int s0 = min(q1, q0 + warp * per), s1 = min(q1, s0 + per);
+    // 2: kept, 1: equal to the boundary key, 0: not kept
+    auto cls = [&](int t) -> int {
+      if (t >= s1) return 0;
+      if (t < c0 || t >= c1) return 2;
+      const uint32_t k = sum_key(sum_at(t));
+      return k > prefix ? 2 : k == prefix ? 1 : 0;
+    };
+    unsigned n_gt = 0, n_eq = 0;
+    for (int t = s0 + lane; t - lane < s1; t += 32) {
+      const int c = cls(t);
+      n_gt += __popc(__ballot_sync(0xffffffffu, c == 2));
+      n_eq += __popc(__ballot_sync(0xffffffffu, c == 1));
+    }
     __syncthreads();
-    unsigned above = 0;
-    for (int x = warp + 1; x < kSelWarps; ++x) above += warp_a[x];
-    const unsigned over = above + v - (a + b);        // candidates in bins above 2 tid + 1
-    if (need > over && need <= over + b) sh_digit = 2 * tid + 1, sh_need = need - over;
-    else if (need > over + b && need <= over + b + a) sh_digit = 2 * tid, sh_need = need - over - b;
-    if (need == 0 && tid == 0) sh_digit = kBins - 1, sh_need = 0;
+    if (lane == 0) warp_a[warp] = n_gt, warp_b[warp] = n_eq;
     __syncthreads();
-    prefix |= (sh_digit & ((1u << bits) - 1u)) << shift;
-    need = sh_need;
+    // kept and equal tokens before this warp's stretch: of the block's warps, of the blocks
+    const unsigned wa = scan_up(warp_a[lane]), wb = scan_up(warp_b[lane]);
+    if (tid == 31) total = make_uint2(wa, wb);
+    cluster_sync();
+    uint2 before = make_uint2(0, 0);
+    for (int c = 0; c < rank; ++c) {
+      const uint2 x = ld_rank(&total, c);
+      before.x += x.x;
+      before.y += x.y;
+    }
+    unsigned eq = before.y + __shfl_sync(0xffffffffu, wb, warp) - n_eq;
+    unsigned at = before.x + __shfl_sync(0xffffffffu, wa, warp) - n_gt + min(eq, need);
+    for (int t = s0 + lane; t - lane < s1; t += 32) {
+      const int c = cls(t);
+      const unsigned m1 = __ballot_sync(0xffffffffu, c == 1);
+      const unsigned ahead = __popc(m1 & ((1u << lane) - 1u));
+      const bool k = c == 2 || (c == 1 && eq + ahead < need);
+      const unsigned mk = __ballot_sync(0xffffffffu, k);
+      if (k) {
+        const unsigned i = at + __popc(mk & ((1u << lane) - 1u));
+        kept[i] = t;
+        if (STAGED) w2[i] = sum_at(t);
+      }
+      at += __popc(mk);
+      eq += __popc(m1);
+    }
   }
-  // need == 0 (nothing but the protected tokens): the key is above every sum
-  if (p.keep == p.sinks + p.recent) prefix = 0xffffffffu;
-  // each warp takes a stretch of positions [s0, s1) of the whole row
-  const int per = (len + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
-  const int s0 = min(len, warp * per), s1 = min(len, s0 + per);
-  // 2: kept, 1: equal to the boundary key, 0: not kept
-  auto cls = [&](int t) -> int {
-    if (t >= s1) return 0;
-    if (t < c0 || t >= c1) return 2;
-    const uint32_t k = key_at(t - c0);
-    return k > prefix ? 2 : k == prefix ? 1 : 0;
-  };
-  unsigned n_gt = 0, n_eq = 0;
-  for (int t = s0 + lane; t - lane < s1; t += 32) {
-    const int c = cls(t);
-    n_gt += __popc(__ballot_sync(0xffffffffu, c == 2));
-    n_eq += __popc(__ballot_sync(0xffffffffu, c == 1));
-  }
-  __syncthreads();
-  if (lane == 0) warp_a[warp] = n_gt, warp_b[warp] = n_eq;
-  __syncthreads();
-  unsigned at = 0, eq = 0;               // kept and equal tokens before this warp's stretch
-  for (int x = 0; x < warp; ++x) at += warp_a[x], eq += warp_b[x];
-  at += min(eq, need);
-  for (int t = s0 + lane; t - lane < s1; t += 32) {
-    const int c = cls(t);
-    const unsigned m1 = __ballot_sync(0xffffffffu, c == 1);
-    const unsigned before = __popc(m1 & ((1u << lane) - 1u));
-    const bool k = c == 2 || (c == 1 && eq + before < need);
-    const unsigned mk = __ballot_sync(0xffffffffu, k);
-    if (k) kept[at + __popc(mk & ((1u << lane) - 1u))] = t;
-    at += __popc(mk);
-    eq += __popc(m1);
-  }
+  // every block of the cluster has read the sums it needs; tokens appended later start at zero
+  cluster_sync();
+  if (STAGED)
+    for (int i = new_len + rank * kSelThreads + tid; i < p.tmax2; i += C * kSelThreads) w2[i] = 0.f;
 }
 
 // Kept rows into another cache: 16 bytes per thread, d / 8 threads per row.
@@ -186,8 +242,8 @@ __global__ void __launch_bounds__(kGThreads) move_kernel(const __grid_constant__
   }
 }
 
-// The kept sums, in order and chunk by chunk as above (source and destination
-// may be one array); zero from the new length on.
+// The kept sums of rows too long for shared memory, in order and chunk by chunk as
+// above (source and destination may be one array); zero from the new length on.
 __global__ void __launch_bounds__(kSelThreads) gather_sums_kernel(const __grid_constant__ EvictCall p) {
   const int u = blockIdx.x;
   const float* src = p.w + (size_t)u * p.tmax;
@@ -222,24 +278,41 @@ cudaError_t launch_rows(const EvictCall& c, cudaLaunchConfig_t& cfg) {
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictCall& c, cudaStream_t s) {
-  cudaError_t e;
-  const int n_c = c.n_tokens - c.sinks - c.recent;      // candidates of the longest row
-  if (n_c <= kStageTok) {
-    const int bytes = n_c > 0 ? n_c * 4 : 0;
-    e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageTok * 4);
-    if (e != cudaSuccess) return e;
-    select_kernel<true><<<c.units, kSelThreads, bytes, s>>>(c);
-  } else {
-    select_kernel<false><<<c.units, kSelThreads, 0, s>>>(c);
-  }
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+cudaError_t launch_evict(const EvictCall& call, cudaStream_t s) {
+  EvictCall c = call;
+  // blocks per unit: while they fit the SMs twice over and have 2048 tokens each, and
+  // as many as the shared memory asks for
+  c.blocks = 1;
+  while (c.blocks < kMaxBlocks && ((c.units * c.blocks * 2 <= 2 * kNumSMs && c.n_tokens / (2 * c.blocks) >= 2048) ||
+                                   c.n_tokens > c.blocks * kStageTok))
+    c.blocks *= 2;
+  const bool staged = c.n_tokens <= c.blocks * kStageTok;
   cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)c.blocks;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)c.units * c.blocks);
+  cfg.blockDim = dim3(kSelThreads);
   cfg.stream = s;
-  cfg.blockDim = dim3(kGThreads);
-  e = c.d == 128 ? launch_rows<128>(c, cfg) : launch_rows<64>(c, cfg);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if (staged) {
+    cfg.dynamicSmemBytes = (size_t)(((c.n_tokens + c.blocks - 1) / c.blocks + 31) & ~31) * sizeof(float);
+    e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageTok * 4);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, select_kernel<true>, c);
+  } else {
+    e = cudaLaunchKernelEx(&cfg, select_kernel<false>, c);
+  }
   if (e != cudaSuccess) return e;
+  // the copies start as the selection ends
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kGThreads);
+  cfg.dynamicSmemBytes = 0;
+  e = c.d == 128 ? launch_rows<128>(c, cfg) : launch_rows<64>(c, cfg);
+  if (e != cudaSuccess || staged) return e;
   gather_sums_kernel<<<c.units, kSelThreads, 0, s>>>(c);
   return cudaGetLastError();
 }

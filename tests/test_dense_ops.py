@@ -880,3 +880,14 @@ def test_prefix_large_calls(bf16, B, T, P):
             ref, tol, _ = _on_gpu(q[b, 4 * h:4 * h + 4], k, v,
                                   torch.ones(4, len(k), dtype=torch.bool, device="cuda"), p.scale, bf16)
             within(_f64(out[b, 4 * h:4 * h + 4]), ref, tol, f"row {b} head {h}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("case", [(1, 1, 64, 400001, None, 150000, 4, 1000, "random"),     # beyond a cluster's shared memory
+                                  (3, 2, 64, 20000, [20000, 8191, 0], 5000, 0, 0, "ties"),   # two blocks and more per head
+                                  (2, 4, 128, 33000, [33000, 4097], 4096, 4096, 0, "random"),
+                                  (40, 8, 64, 4100, None, 100, 3, 50, "same")],
+                         ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_evict_long_rows(case, in_place):
+    test_evict_exact(case, in_place)
