@@ -187,7 +187,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     for (int i = new_len + rank * kSelThreads + tid; i < p.tmax2; i += C * kSelThreads) w2[i] = 0.f;
 }
 
-// Kept rows into another cache: 16 bytes per thread, d / 8 threads per row.
+// Kept rows into another cache: 16 bytes per thread, d / 8 threads per row.  Rows
+// that are kept whatever the sums are (the protected ones, or all of a short row's)
+// do not wait for the selection.
 constexpr int kGThreads = 256;
 constexpr int kGUnroll = 8;
 
@@ -199,18 +201,33 @@ __global__ void __launch_bounds__(kGThreads) gather_kernel(const __grid_constant
   const uint4* src = reinterpret_cast<const uint4*>(b >= nb ? p.v : p.k) + (size_t)u * p.tmax * TPR + col;
   uint4* dst = reinterpret_cast<uint4*>(b >= nb ? p.v2 : p.k2) + (size_t)u * p.tmax2 * TPR + col;
   const int i0 = b % nb * RPB * kGUnroll + threadIdx.x / TPR;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int* kept = p.kept + (size_t)u * p.keep;
+  const int len = evict_len(p, u), new_len = min(len, p.keep);
+  const bool all = len <= p.keep;
   int t[kGUnroll];
   uint4 x[kGUnroll];
+  bool wait = false;
 #pragma unroll
-  for (int k = 0; k < kGUnroll; ++k) t[k] = i0 + k * RPB < p.keep ? kept[i0 + k * RPB] : -1;
-#pragma unroll
-  for (int k = 0; k < kGUnroll; ++k)
+  for (int k = 0; k < kGUnroll; ++k) {
+    const int i = i0 + k * RPB;
+    t[k] = i >= new_len ? -1 : all || i < p.sinks ? i : i >= new_len - p.recent ? len - new_len + i : -2;
+    wait = wait || t[k] == -2;
     if (t[k] >= 0) x[k] = src[(size_t)t[k] * TPR];
+  }
+  if (wait) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int* kept = p.kept + (size_t)u * p.keep;
+    int q[kGUnroll];
+#pragma unroll
+    for (int k = 0; k < kGUnroll; ++k) q[k] = t[k] == -2 ? kept[i0 + k * RPB] : -1;
+#pragma unroll
+    for (int k = 0; k < kGUnroll; ++k)
+      if (q[k] >= 0) x[k] = src[(size_t)q[k] * TPR];
+  }
 #pragma unroll
   for (int k = 0; k < kGUnroll; ++k)
-    if (t[k] >= 0) dst[(size_t)(i0 + k * RPB) * TPR] = x[k];
+    if (t[k] != -1) dst[(size_t)(i0 + k * RPB) * TPR] = x[k];
+  // this kernel's end is the call's end: not before the selection's
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Kept rows moved down within one cache.  A block owns a 64-byte column of a

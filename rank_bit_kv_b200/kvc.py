@@ -194,12 +194,12 @@ class Layout:
         check(lib().kvc_create_layout(C.byref(desc), C.byref(h)))
         self.h = h
         self.desc = desc
-        self._sizes = None
         # (layers, batch, query heads, KV heads, head dim, max_tokens, bf16 output) of a dense layout
         self._dense = None
         if desc.kind == KVC_DENSE_BF16:
             self._dense = (max(1, desc.n_layers), desc.batch, desc.n_q_heads, desc.n_kv_heads, desc.head_dim,
                            desc.max_tokens, bool(desc.out_bf16))
+            self._dense_bytes = self.buffer_sizes()["k_dense"]
 
     def __del__(self):
         if getattr(self, "h", None) and _lib is not None:
@@ -210,12 +210,6 @@ class Layout:
         arr = (C.c_size_t * NBUF)()
         check(lib().kvc_buffer_sizes(self.h, arr))
         return dict(zip(BUFS, list(arr)))
-
-    def buffer_sizes_cached(self):
-        """buffer_sizes(), asked once (a layout is immutable)."""
-        if self._sizes is None:
-            self._sizes = self.buffer_sizes()
-        return self._sizes
 
     def workspace_bytes(self, n_tokens):
         return int(lib().kvc_workspace_bytes(self.h, n_tokens))
@@ -519,11 +513,6 @@ def block_compact(src_layout, src_cache, dst_layout, dst_cache, kept, stream=Non
 # `stream` is a cudaStream_t (default: torch's current stream of that device).
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
 def _tensor(t, name, dtype, shape, device):
     """t's address, after the checks that the C ABI cannot make."""
     if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
@@ -538,10 +527,11 @@ def _run(device, stream, call, *args):
 
     if device.type != "cuda":
         raise ValueError(f"the tensors are on {device}, not on a GPU")
-    if device.index != torch._C._cuda_getDevice():
+    index = device.index
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _run(device, stream, call, *args)
-    status = call(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream)
+    status = call(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
     if status:
         check(status)
 
@@ -557,21 +547,22 @@ def _dense_dims(layout, cache):
             torch.bfloat16 if bf16 else torch.float32)
 
 
-def _dense_cache(cache, device, batch):
-    """The cache's C struct, after checks of its buffers."""
-    import torch
-
-    sizes = cache.layout.buffer_sizes_cached()
-    k, v = cache.bufs["k_dense"], cache.bufs["v_dense"]
-    for name, t in (("k_dense", k), ("v_dense", v)):
-        if t.device != device or t.nbytes < sizes[name] or not t.is_contiguous():
-            raise ValueError(f"cache.{name} must be a contiguous buffer of {sizes[name]} bytes on {device}")
+def _dense_cache(layout, cache, device, batch):
+    """The cache's C struct, after checks of its buffers against the layout."""
+    need = layout._dense_bytes
     c = CacheDesc()
+    bufs = cache.bufs
+    k, v = bufs["k_dense"], bufs["v_dense"]
+    if not (k.device == device == v.device and k.nbytes >= need <= v.nbytes and k.is_contiguous()
+            and v.is_contiguous()):
+        raise ValueError(f"cache.k_dense and v_dense must be contiguous buffers of {need} bytes on {device}")
     c.k_dense = k.data_ptr()
     c.v_dense = v.data_ptr()
     c.n_tokens = cache.n_tokens
     c.layer = cache.layer
     if cache.seq_lens is not None:
+        import torch
+
         c.seq_lens = _tensor(cache.seq_lens, "cache.seq_lens", torch.int32, (batch,), device)
     return c
 
@@ -591,12 +582,13 @@ def window_attn(layout: Layout, cache: Cache, q, out, ws, window, sinks=0, strea
 
     lead, B, Hq, _, d, _, out_type = _dense_dims(layout, cache)
     dev = q.device
-    _need(q.dim() == 4 + len(lead), "q must be [B, Hq, n_q, d] (all layers at once: [n_layers, B, Hq, n_q, d])")
+    if q.dim() != 4 + len(lead):
+        raise ValueError("q must be [B, Hq, n_q, d] (all layers at once: [n_layers, B, Hq, n_q, d])")
     n_q = q.shape[-2]
     shape = (*lead, B, Hq, n_q, d)
     qp = _tensor(q, "q", torch.bfloat16, shape, dev)
     op = _tensor(out, "out", out_type, shape, dev)
-    c = _dense_cache(cache, dev, B)
+    c = _dense_cache(layout, cache, dev, B)
     _run(dev, stream, lib().kvc_window_attn, layout.h, c, qp, n_q, window, sinks, op, *_workspace(ws, dev))
 
 
@@ -611,7 +603,7 @@ def decode_accum(layout: Layout, cache: Cache, q, weights, out, ws, stream=None)
     qp = _tensor(q, "q", torch.bfloat16, shape, dev)
     op = _tensor(out, "out", out_type, shape, dev)
     ap = _tensor(weights, "weights", torch.float32, (*lead, B, Hkv, cap), dev)
-    c = _dense_cache(cache, dev, B)
+    c = _dense_cache(layout, cache, dev, B)
     _run(dev, stream, lib().kvc_decode_accum, layout.h, c, qp, ap, op, *_workspace(ws, dev))
 
 
@@ -629,8 +621,8 @@ def evict(src_layout: Layout, src_cache: Cache, dst_layout: Layout, dst_cache: C
     dev = weights.device
     ap = _tensor(weights, "weights", torch.float32, (*lead, B, Hkv, cap), dev)
     bp = _tensor(dst_weights, "dst_weights", torch.float32, (*lead2, B2, Hkv2, cap2), dev)
-    a = _dense_cache(src_cache, dev, B)
-    b = _dense_cache(dst_cache, dev, B2)
+    a = _dense_cache(src_layout, src_cache, dev, B)
+    b = _dense_cache(dst_layout, dst_cache, dev, B2)
     kept = torch.empty((*lead, B, Hkv, max(0, int(keep))), dtype=torch.int32, device=dev)
     lens = torch.empty((B,), dtype=torch.int32, device=dev)
     _run(dev, stream, lib().kvc_evict, src_layout.h, a, dst_layout.h, b, ap, bp, keep, sinks, recent,
@@ -651,6 +643,6 @@ def prefix_decode(prefix_layout: Layout, prefix_cache: Cache, layout: Layout, ca
     dev, shape = q.device, (*lead, B, Hq, d)
     qp = _tensor(q, "q", torch.bfloat16, shape, dev)
     op = _tensor(out, "out", out_type, shape, dev)
-    a = _dense_cache(prefix_cache, dev, 1)
-    b = _dense_cache(cache, dev, B)
+    a = _dense_cache(prefix_layout, prefix_cache, dev, 1)
+    b = _dense_cache(layout, cache, dev, B)
     _run(dev, stream, lib().kvc_prefix_decode, prefix_layout.h, a, layout.h, b, qp, op, *_workspace(ws, dev))
