@@ -21,7 +21,7 @@
 namespace kvc {
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;              // 11 bits a pass: 11 + 11 + 10
 constexpr int kStageTok = 48 * 1024;     // sums held in a block's shared memory
@@ -29,6 +29,11 @@ constexpr int kMaxBlocks = 8;            // blocks of a cluster
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void add_rank(unsigned* p, unsigned x, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
 }
 __device__ __forceinline__ uint2 ld_rank(const void* p, int rank) {
   uint32_t a;
@@ -60,9 +65,10 @@ __device__ __forceinline__ uint32_t sum_key(float w) { return w > 0.f ? __float_
 template <bool STAGED>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictCall p) {
   extern __shared__ float sums[];        // STAGED: the block's stretch of the row's sums
-  __shared__ __align__(8) unsigned hist[2][kBins];
+  __shared__ __align__(16) unsigned hist[kBins], all[2][kBins];      // the block's counts; block 0: the cluster's
   __shared__ unsigned warp_a[kSelWarps], warp_b[kSelWarps];
-  __shared__ unsigned sh_digit, sh_need;
+  __shared__ uint2 sh_digit;             // block 0: the digit found, and need
+  static_assert(kBins == 4 * kSelThreads && kSelWarps <= 32, "a thread owns four bins");
   __shared__ uint2 total;                // this block's kept tokens, and those equal to the boundary
   const int C = p.blocks, rank = blockIdx.x % C, u = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -95,43 +101,56 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     // need becomes the number of candidates equal to it that are kept
     uint32_t prefix = 0;
     int shift = 32;
-    for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(&hist[4 * tid]) = *reinterpret_cast<uint4*>(&all[0][4 * tid]) = none;
     for (int pass = 0; pass < 3; ++pass) {
       const int bits = pass == 2 ? 10 : 11;
       const uint32_t hi = pass == 0 ? 0u : ~0u << shift;
-      unsigned* const mine = hist[pass & 1];
+      unsigned* const sum = all[pass & 1];
       shift -= bits;
       __syncthreads();
       for (int t = h0 + tid; t < h1; t += kSelThreads) {
         const uint32_t k = sum_key(sum_at(t));
-        if ((k & hi) == prefix) atomicAdd(&mine[(k >> shift) & ((1u << bits) - 1u)], 1u);
+        if ((k & hi) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+      }
+      if (pass == 0) cluster_sync();     // the cluster's blocks run, block 0's counts are zero
+      else __syncthreads();
+      // counts to block 0, few of them: the sums share most of their leading bits.  (Every
+      // block reading all of them: 25 us for 8 rows of 32K tokens where this takes 23.)
+      const uint4 x = *reinterpret_cast<const uint4*>(&hist[4 * tid]);
+      *reinterpret_cast<uint4*>(&hist[4 * tid]) = none;
+      if (x.x) add_rank(&sum[4 * tid], x.x, 0);
+      if (x.y) add_rank(&sum[4 * tid + 1], x.y, 0);
+      if (x.z) add_rank(&sum[4 * tid + 2], x.z, 0);
+      if (x.w) add_rank(&sum[4 * tid + 3], x.w, 0);
+      cluster_sync();
+      if (rank == 0) {
+        *reinterpret_cast<uint4*>(&all[(pass + 1) & 1][4 * tid]) = none;
+        // suffix sums of the bins: thread t owns bins 4 t .. 4 t + 3
+        const uint4 y = *reinterpret_cast<const uint4*>(&sum[4 * tid]);
+        const unsigned bin[4] = {y.x, y.y, y.z, y.w};
+        const unsigned own = bin[0] + bin[1] + bin[2] + bin[3];
+        unsigned v = own;                // sum over this lane and the lanes above it
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned z = __shfl_down_sync(0xffffffffu, v, o);
+          if (lane + o < 32) v += z;
+        }
+        if (lane == 0) warp_a[warp] = v;
+        __syncthreads();
+        const unsigned above = __reduce_add_sync(0xffffffffu, lane > warp && lane < kSelWarps ? warp_a[lane] : 0u);
+        unsigned over = above + v - own; // candidates in the bins above
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          if (need > over && need <= over + bin[k]) sh_digit = make_uint2(4 * tid + k, need - over);
+          over += bin[k];
+        }
+        if (need == 0 && tid == 0) sh_digit = make_uint2(kBins - 1, 0u);
       }
       cluster_sync();
-      // the other histogram is not read any more: zero for the next pass
-      hist[(pass + 1) & 1][2 * tid] = hist[(pass + 1) & 1][2 * tid + 1] = 0;
-      // suffix sums of the cluster's bins: thread t owns bins 2t, 2t + 1
-      unsigned a = 0, b = 0;
-      for (int c = 0; c < C; ++c) {
-        const uint2 x = ld_rank(&mine[2 * tid], c);
-        a += x.x;
-        b += x.y;
-      }
-      unsigned v = a + b;                // sum over this lane and the lanes above it
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned x = __shfl_down_sync(0xffffffffu, v, o);
-        if (lane + o < 32) v += x;
-      }
-      if (lane == 0) warp_a[warp] = v;
-      __syncthreads();
-      const unsigned above = __reduce_add_sync(0xffffffffu, lane > warp ? warp_a[lane] : 0u);
-      const unsigned over = above + v - (a + b);        // candidates in bins above 2 tid + 1
-      if (need > over && need <= over + b) sh_digit = 2 * tid + 1, sh_need = need - over;
-      else if (need > over + b && need <= over + b + a) sh_digit = 2 * tid, sh_need = need - over - b;
-      if (need == 0 && tid == 0) sh_digit = kBins - 1, sh_need = 0;
-      __syncthreads();
-      prefix |= (sh_digit & ((1u << bits) - 1u)) << shift;
-      need = sh_need;
+      const uint2 found = ld_rank(&sh_digit, 0);
+      prefix |= (found.x & ((1u << bits) - 1u)) << shift;
+      need = found.y;
     }
     // need == 0 (nothing but the protected tokens): the key is above every sum
     if (p.keep == p.sinks + p.recent) prefix = 0xffffffffu;
@@ -155,7 +174,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     if (lane == 0) warp_a[warp] = n_gt, warp_b[warp] = n_eq;
     __syncthreads();
     // kept and equal tokens before this warp's stretch: of the block's warps, of the blocks
-    const unsigned wa = scan_up(warp_a[lane]), wb = scan_up(warp_b[lane]);
+    const unsigned wa = scan_up(lane < kSelWarps ? warp_a[lane] : 0u), wb = scan_up(lane < kSelWarps ? warp_b[lane] : 0u);
     if (tid == 31) total = make_uint2(wa, wb);
     cluster_sync();
     uint2 before = make_uint2(0, 0);
@@ -187,9 +206,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     for (int i = new_len + rank * kSelThreads + tid; i < p.tmax2; i += C * kSelThreads) w2[i] = 0.f;
 }
 
-// Kept rows into another cache: 16 bytes per thread, d / 8 threads per row.  Rows
-// that are kept whatever the sums are (the protected ones, or all of a short row's)
-// do not wait for the selection.
+// Kept rows into another cache: 16 bytes per thread, d / 8 threads per row.  (Copying
+// the protected rows before the selection ends takes longer in all: 121 us for 8 rows
+// of 32K tokens, 112 so.)
 constexpr int kGThreads = 256;
 constexpr int kGUnroll = 8;
 
@@ -201,33 +220,18 @@ __global__ void __launch_bounds__(kGThreads) gather_kernel(const __grid_constant
   const uint4* src = reinterpret_cast<const uint4*>(b >= nb ? p.v : p.k) + (size_t)u * p.tmax * TPR + col;
   uint4* dst = reinterpret_cast<uint4*>(b >= nb ? p.v2 : p.k2) + (size_t)u * p.tmax2 * TPR + col;
   const int i0 = b % nb * RPB * kGUnroll + threadIdx.x / TPR;
-  const int len = evict_len(p, u), new_len = min(len, p.keep);
-  const bool all = len <= p.keep;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int* kept = p.kept + (size_t)u * p.keep;
   int t[kGUnroll];
   uint4 x[kGUnroll];
-  bool wait = false;
 #pragma unroll
-  for (int k = 0; k < kGUnroll; ++k) {
-    const int i = i0 + k * RPB;
-    t[k] = i >= new_len ? -1 : all || i < p.sinks ? i : i >= new_len - p.recent ? len - new_len + i : -2;
-    wait = wait || t[k] == -2;
-    if (t[k] >= 0) x[k] = src[(size_t)t[k] * TPR];
-  }
-  if (wait) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int* kept = p.kept + (size_t)u * p.keep;
-    int q[kGUnroll];
-#pragma unroll
-    for (int k = 0; k < kGUnroll; ++k) q[k] = t[k] == -2 ? kept[i0 + k * RPB] : -1;
-#pragma unroll
-    for (int k = 0; k < kGUnroll; ++k)
-      if (q[k] >= 0) x[k] = src[(size_t)q[k] * TPR];
-  }
+  for (int k = 0; k < kGUnroll; ++k) t[k] = i0 + k * RPB < p.keep ? kept[i0 + k * RPB] : -1;
 #pragma unroll
   for (int k = 0; k < kGUnroll; ++k)
-    if (t[k] != -1) dst[(size_t)(i0 + k * RPB) * TPR] = x[k];
-  // this kernel's end is the call's end: not before the selection's
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (t[k] >= 0) x[k] = src[(size_t)t[k] * TPR];
+#pragma unroll
+  for (int k = 0; k < kGUnroll; ++k)
+    if (t[k] >= 0) dst[(size_t)(i0 + k * RPB) * TPR] = x[k];
 }
 
 // Kept rows moved down within one cache.  A block owns a 64-byte column of a

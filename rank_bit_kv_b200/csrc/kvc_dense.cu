@@ -149,6 +149,7 @@ char* plan_prefix(const kvc_layout* L, kvc::DenseAttn* p, kvc::DenseAttn* pre, v
   char* const end = take_plan(pre, kvc::dense_plan(pre->units, pre->rows, 1, p->d, pre->n_tokens, p->out_bf16, kvc::kFlatMerge), true, at);
   p->pre = pre->own;
   p->pre_batch = L->d.batch;
+  if (pre->tensor) p->clear_err = 0;     // the first kernel has cleared the error word
   return end;
 }
 
@@ -207,6 +208,7 @@ extern "C" kvc_status kvc_decode_accum(const kvc_layout* L, const kvc_cache* c, 
   kvc::DenseAttn p;
   kvc_status st = dense_problem(what, L, c, 1, &p);
   if (st != KVC_OK || (st = check_io(what, q, out)) != KVC_OK) return st;
+  if (kvc_accum_workspace_bytes(L, c->n_tokens) == 0) return report_error(KVC_EUNSUPPORTED, "%s: too many query rows", what);
   if (!aligned16(weights)) return report_error(KVC_EALIGN, "%s: weights must be 16-byte aligned", what);
   if ((st = check_ws(what, workspace, ws_size, kvc_accum_workspace_bytes(L, c->n_tokens))) != KVC_OK) return st;
   p.q = (const __nv_bfloat16*)q;
@@ -242,8 +244,9 @@ extern "C" kvc_status kvc_prefix_decode(const kvc_layout* PL, const kvc_cache* p
     return report_error(KVC_EINVAL, "%s: the two layouts differ in heads, head_dim or layers", what);
   if (PL->scale != L->scale) return report_error(KVC_EINVAL, "%s: the two layouts differ in softmax_scale", what);
   if ((st = check_io(what, q, out)) != KVC_OK) return st;
-  if ((st = check_ws(what, workspace, ws_size, kvc_prefix_workspace_bytes(L, c->n_tokens, pc->n_tokens))) != KVC_OK)
-    return st;
+  const size_t need = kvc_prefix_workspace_bytes(L, c->n_tokens, pc->n_tokens);
+  if (need == 0) return report_error(KVC_EUNSUPPORTED, "%s: too many query rows", what);
+  if ((st = check_ws(what, workspace, ws_size, need)) != KVC_OK) return st;
   p.q = pre.q = (const __nv_bfloat16*)q;
   p.out = pre.out = out;
   if ((st = check_end(what, workspace, ws_size, plan_prefix(L, &p, &pre, workspace))) != KVC_OK) return st;

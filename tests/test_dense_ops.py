@@ -891,3 +891,93 @@ def test_prefix_large_calls(bf16, B, T, P):
                          ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
 def test_evict_long_rows(case, in_place):
     test_evict_exact(case, in_place)
+
+
+def test_calls_refuse_more_rows_than_an_index_holds():
+    L = kvc.lib()
+    f = C.c_void_p(F)
+    wide = dense(B=256, Hq=4096 * 64, Hkv=64, T=64, L=64)
+    assert L.kvc_accum_workspace_bytes(wide.h, 64) == 0 and L.kvc_prefix_workspace_bytes(wide.h, 64, 64) == 0
+    assert _status(L.kvc_decode_accum(wide.h, C.byref(_cs(64)), f, f, f, f, BIG, None)) == "KVC_EUNSUPPORTED"
+    pre = dense(B=1, Hq=4096 * 64, Hkv=64, T=64, L=64)
+    assert _status(L.kvc_prefix_decode(pre.h, C.byref(_cs(64)), wide.h, C.byref(_cs(64)), f, f, f, BIG,
+                                       None)) == "KVC_EUNSUPPORTED"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bf16", [0, 1])
+def test_empty_cache_gives_zeros(bf16):
+    import torch
+
+    p = Problem(2, 8, 2, 128, 64, bf16=bf16, seed=60)
+    p.k.fill_(float("nan"))
+    p.v.fill_(float("nan"))
+    p.cache.n_tokens = 0
+    for n_q in (1, 3, 60):
+        q, out = p.queries(n_q)
+        p.window(q, out, 8, 2)
+        assert (out == 0).all()
+    q, out = p.queries()
+    w = torch.full((2, 2, 64), 3.0, device="cuda")
+    kvc.decode_accum(p.layout, p.cache, q, w, out, p.ws(p.layout.accum_workspace_bytes(0)))
+    assert (out == 0).all() and (w == 3).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [2, 40])
+def test_prefix_non_finite_own_token_stays_in_its_row(rows):
+    """A NaN value of one row's own token, an infinite query of another: nobody else's output notices."""
+    p = Problem(rows, 8, 2, 128, 20, cap=24, bf16=1, seed=61)
+    pre = Problem(1, 8, 2, 128, 300, seed=62)
+    q, out = p.queries()
+    p.v[0, 1, 7, 3] = float("nan")
+    q[1, 0, 5] = float("inf")
+    kvc.prefix_decode(pre.layout, pre.cache, p.layout, p.cache, q, out, p.ws(p.layout.prefix_workspace_bytes(20, 300)))
+    got = _f64(out)
+    assert np.isnan(got[0, 4:, 3]).all() and not np.isfinite(got[1, 0]).any()
+    v, qq = _f64(p.v), _f64(q)
+    v[0, 1, 7, 3], qq[1, 0, 5] = 0.0, 0.0
+    ref, tol = D.prefix_attention(qq, _f64(pre.k)[0], _f64(pre.v)[0], _f64(p.k), v, p.lens, p.scale, True, 8)
+    clean = np.ones(got.shape, bool)
+    clean[0, 4:, 3] = clean[1, 0] = False
+    within(got[clean], ref[clean], tol[clean])
+
+
+@pytest.mark.gpu
+def test_window_scores_that_outgrow_the_reference():
+    """Scores that keep rising along the tokens, by far more than 2^24 a tile, and fall again."""
+    p = Problem(1, 4, 1, 64, 900, bf16=1, seed=63)
+    q, out = p.queries(300)
+    import torch
+
+    t = np.concatenate([np.linspace(0, 60, 600), np.linspace(60, -60, 300)])
+    q += 2.0
+
+    p.k[0, 0] = (p.k[0, 0].float() * 0.1 + torch.tensor(t, device="cuda").float()[:, None] / 4).bfloat16()
+    for W in (900, 250):
+        p.window(q, out, W, 3)
+        ref, tol = D.window_attention(_f64(q), _f64(p.k), _f64(p.v), p.lens, W, 3, p.scale, True, 8)
+        within(_f64(out), ref, tol, f"window {W}")
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams_at_once():
+    import torch
+
+    ps = [Problem(2, 16, 2, 128, 1200, [1200, 700], bf16=1, seed=70 + i) for i in range(2)]
+    io = [p.queries(96) for p in ps]
+    want = []
+    for p, (q, o) in zip(ps, io):
+        p.window(q, o, 300, 4)
+        want.append(o.clone())
+        o.zero_()
+    ws = [p.ws(p.layout.window_workspace_bytes(1200, 96)) for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, (q, o), w, s in zip(ps, io, ws, streams):
+            with torch.cuda.stream(s):
+                p.window(q, o, 300, 4, w)
+    torch.cuda.synchronize()
+    for (_, o), ref in zip(io, want):
+        assert torch.equal(o, ref)
