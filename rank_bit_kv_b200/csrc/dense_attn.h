@@ -57,6 +57,7 @@ struct DenseAttn {
   int clear_err;                // the kernel clears it first
   int tensor;                   // the tcgen05 kernel
   int wide;                     // blocks of eight warps, one per SM
+  int no_copies;                // test switch: the tcgen05 kernel loads no tiles, its waits run out
 };
 
 // Tokens that row unit u holds.

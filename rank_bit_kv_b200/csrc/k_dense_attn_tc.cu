@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpTma) {
     // ---- K / V tiles into the ring
-    if (lane == 0 && n > 0) {
+    if (lane == 0 && n > 0 && !p.no_copies) {
       int pos = 0, issued = 0;
       bool ok = true;
       auto load = [&](const CUtensorMap* map, int t) {

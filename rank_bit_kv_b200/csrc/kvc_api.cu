@@ -111,6 +111,8 @@ kvc_status kvc::report_error(kvc_status st, const char* fmt, ...) {
   return st;
 }
 
+int kvc::test_no_copies() { return g_test_no_copies; }
+
 extern "C" {
 
 const char* kvc_last_error(void) { return g_err.c_str(); }

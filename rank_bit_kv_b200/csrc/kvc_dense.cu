@@ -96,6 +96,7 @@ char* take_plan(kvc::DenseAttn* p, const kvc::DensePlan& f, bool partials, char*
   p->own.blocks = f.blocks;
   p->own.splits = f.splits;
   p->wide = f.wide;
+  p->no_copies = kvc::test_no_copies();
   p->own.flat = f.flat;
   p->own.Hkv = p->Hkv;
   p->own.layers = p->units / (p->Hkv * p->len_rows);

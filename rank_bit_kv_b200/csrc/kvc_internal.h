@@ -223,6 +223,9 @@ cudaError_t launch_compact(const uint8_t* src_codes, const __half* src_scales, u
 // Record a status and message for kvc_last_error(); returns st.
 kvc_status report_error(kvc_status st, const char* fmt, ...);
 
+// The calling thread's kvc_test_skip_tile_copies switch.
+int test_no_copies();
+
 // kernel launchers (return the cudaGetLastError of the launch)
 cudaError_t launch_qproj(const Params& p, cudaStream_t s);
 cudaError_t launch_split(const Params& p, cudaStream_t s);

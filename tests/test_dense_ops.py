@@ -981,3 +981,25 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for (_, o), ref in zip(io, want):
         assert torch.equal(o, ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n_q,Hq", [(150, 8), (20, 8), (600, 32)])
+def test_bounded_waits_give_up_report_and_leave_the_context_usable(n_q, Hq):
+    import torch
+
+    p = Problem(1, Hq, 2, 128, 700, bf16=1, seed=80)
+    q, out = p.queries(n_q)
+    lib = kvc.lib()
+    lib.kvc_test_skip_tile_copies(1)
+    try:
+        ws = p.window(q, out, 400, 4)                       # the waits run out (0.5 s) and the blocks end
+        torch.cuda.synchronize()
+    finally:
+        lib.kvc_test_skip_tile_copies(0)
+    assert int(ws[:4].view(torch.int32)) & kvc.DEV_WAIT_TIMEOUT
+    p.window(q, out, 400, 4, ws)
+    torch.cuda.synchronize()
+    assert int(ws[:4].view(torch.int32)) == 0
+    ref, tol = D.window_attention(_f64(q)[:, :1], _f64(p.k)[:, :1], _f64(p.v)[:, :1], p.lens, 400, 4, p.scale, True, 8)
+    within(_f64(out)[:, :1], ref, tol)
