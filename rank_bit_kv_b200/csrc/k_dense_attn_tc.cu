@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_here = min(32, n_rows - (r - lane));       // rows of this warp
       bool fine = true;
       if (ok && p.finish) {
-#pragma unroll
+#pragma unroll 2
         for (int c = 0; c < D; c += 16) {
           float f[16];
           values(c, f);
@@ -616,9 +616,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k < n_here) reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + to)[c] = *chunk(k, c);
         }
       } else if (ok) {
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += D / 2) {
-#pragma unroll
+#pragma unroll 2
           for (int c = 0; c < D / 2; c += 16) {
             float f[16];
             values(c0 + c, f);
