@@ -321,7 +321,9 @@ cudaError_t launch_evict(const EvictCall& call, cudaStream_t s) {
   cudaError_t e;
   if (staged) {
     cfg.dynamicSmemBytes = (size_t)(((c.n_tokens + c.blocks - 1) / c.blocks + 31) & ~31) * sizeof(float);
-    e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageTok * 4);
+    e = cudaSuccess;
+    if (cfg.dynamicSmemBytes > 16 * 1024)                // with the histograms above what every kernel may have
+      e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageTok * 4);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, select_kernel<true>, c);
   } else {
     e = cudaLaunchKernelEx(&cfg, select_kernel<false>, c);

@@ -623,8 +623,8 @@ def evict(src_layout: Layout, src_cache: Cache, dst_layout: Layout, dst_cache: C
     bp = _tensor(dst_weights, "dst_weights", torch.float32, (*lead2, B2, Hkv2, cap2), dev)
     a = _dense_cache(src_layout, src_cache, dev, B)
     b = _dense_cache(dst_layout, dst_cache, dev, B2)
-    kept = torch.empty((*lead, B, Hkv, max(0, int(keep))), dtype=torch.int32, device=dev)
-    lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    kept = weights.new_empty((*lead, B, Hkv, max(0, int(keep))), dtype=torch.int32)
+    lens = weights.new_empty((B,), dtype=torch.int32)
     _run(dev, stream, lib().kvc_evict, src_layout.h, a, dst_layout.h, b, ap, bp, keep, sinks, recent,
          kept.data_ptr() or None, lens.data_ptr())
     return kept, lens
