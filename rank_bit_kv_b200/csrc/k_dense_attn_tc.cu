@@ -19,6 +19,12 @@
 // Otherwise (up to 128 rows, or too few blocks to fill the SMs) they are the
 // same 128 rows over the even and the odd tiles, merged through shared memory.
 //
+// A prompt of 8192 tokens, window 2048, 32/8 heads of 128: 272 us, 885 TFLOP/s of what its
+// queries see.  What is left is a stream's chain of softmax, P V and Q K^T, which two
+// streams overlap by half; TMEM has no room for a third.  Measured and not kept: two
+// threads per row, which exchange maxima (327 us where one thread took 320); 64-token
+// tiles with two score buffers per stream, whose Q K^T runs at half rate (343).
+//
 // P is rounded to bf16, the output's own precision, as V's type asks (both
 // operands of an MMA have one type); sums are taken before the rounding.
 #include <cuda.h>
@@ -214,6 +220,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the error word is cleared by the first block; a wait gives up only much later
   if (p.clear_err && blockIdx.x == 0 && threadIdx.x == 0) *err = 0u;
 
+  if (warp < kWarpMma) {
+    // queries: a warp its rows, neighbouring lanes the chunks of one (a row per lane
+    // takes 4000 clocks more of the copies' issue); zero past the block's rows
+    constexpr int RPW = RB / 8, CPR = D / 8, RPI = 32 / CPR;
+    const int mine = warp * RPW + lane % RPW;
+    const long long off = dense_row_at(p, u, r0 + min(mine, n_rows - 1));
+#pragma unroll
+    for (int i = 0; i < RPW / RPI; ++i) {
+      const int k = i * RPI + lane / CPR, r = warp * RPW + k, c = lane % CPR;
+      const __nv_bfloat16* src = p.q + __shfl_sync(0xffffffffu, off, k) + c * 8;
+      cp_async16(sm_q + (r / kTM) * C::kTileB + (c / 8) * C::kHalfB + (r % kTM) * 128 + (((c & 7) ^ (r & 7)) << 4), src,
+                 r < n_rows ? 16 : 0);
+    }
+  }
   if (threadIdx.x == 0) {
     mbar_init(&bars.q_full, kSoftThreads / 32);
     for (int i = 0; i < NST; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
@@ -391,24 +411,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = warp >> 2;
     const int row = (warp & 3) * 32 + lane;              // row of the stream = TMEM lane
     const uint32_t tl_base = tmem + ((uint32_t)(warp & 3) << 21);
-    if (n > 0) {
-      // queries: a warp its rows, neighbouring lanes the chunks of one (a row per lane
-      // takes 4000 clocks more of the copies' issue); zero past the block's rows
-      constexpr int RPW = RB / 8, CPR = D / 8, RPI = 32 / CPR;
-      const int mine = warp * RPW + lane % RPW;
-      const long long off = dense_row_at(p, u, r0 + min(mine, n_rows - 1));
-#pragma unroll
-      for (int i = 0; i < RPW / RPI; ++i) {
-        const int k = i * RPI + lane / CPR, r = warp * RPW + k, c = lane % CPR;
-        const __nv_bfloat16* src = p.q + __shfl_sync(0xffffffffu, off, k) + c * 8;
-        cp_async16(sm_q + (r / kTM) * C::kTileB + (c / 8) * C::kHalfB + (r % kTM) * 128 + (((c & 7) ^ (r & 7)) << 4), src,
-                   r < n_rows ? 16 : 0);
-      }
-      cp_async_wait_all();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.q_full);
-    }
+    cp_async_wait_all();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.q_full);
+    if (n == 0) named_bar(1, kSoftThreads);              // nothing else waits for the copies' end
     const int r = (PAIR ? s * kTM : 0) + row;            // row of the block
     const int pos = dense_row_pos(p, len, r0 + min(r, n_rows - 1));
     // positions of the stream's rows
