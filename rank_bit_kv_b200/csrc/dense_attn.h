@@ -56,6 +56,7 @@ struct DenseAttn {
   uint32_t* err;                // error word (bounded waits)
   int clear_err;                // the kernel clears it first
   int tensor;                   // the tcgen05 kernel
+  int solo;                     // of it: blocks of one stream
   int wide;                     // blocks of eight warps, one per SM
   int no_copies;                // test switch: the tcgen05 kernel loads no tiles, its waits run out
 };
@@ -106,7 +107,7 @@ constexpr int kFlatFrom = 32768;         // 8 KB tiles from which a call goes fl
 constexpr int kFlatMerge = 6144;         // and where there is a second kernel anyway
 
 struct DensePlan {
-  int tensor, flat, wide, row_block, blocks, splits;
+  int tensor, solo, flat, wide, row_block, blocks, splits;
   long long slots;              // partials, of row_block rows each
 };
 DensePlan dense_plan(int units, int group, int n_q, int d, long long tokens, int out_bf16, int flat_from);

@@ -26,6 +26,11 @@ using namespace tc;
 
 constexpr int kTok = 16;                 // tokens per tile
 constexpr int kSlots = 2 * kNumSMs;      // two blocks per SM
+// Tiles of 128 tokens up to which the tcgen05 kernel takes one stream per block: with
+// few, the blocks' beginnings and ends count (prompts of 795, window 238: 97 us, 115 in
+// pairs; 9 tiles: 183 and 179); with many, K and V are read twice as often (18 tiles: 283
+// and 271), which at d = 64 costs half as much (25 tiles: 132 and 138).
+constexpr int solo_tiles(int d) { return d == 64 ? 32 : 6; }
 constexpr int kMaxSmem = 216 * 1024;     // dynamic shared memory of a block, at most
 
 enum Mode { kOneToken = 0, kManyTokens = 1, kScores = 2 };
@@ -983,9 +988,10 @@ int warp_splits(long long blocks, long long tokens) {
 
 // The kernel and the split of a problem's tokens (group: query rows per token).
 //
-// tcgen05 kernel: bf16 output and at least kTensorRows rows per KV head.  256 rows
-// per block where rows and tokens give every SM a block, 128 otherwise; splits of
-// at least two tiles per score stream up to one block per SM.
+// tcgen05 kernel: bf16 output and at least kTensorRows rows per KV head.  Blocks of one
+// stream where they fill the SMs twice and have few tiles; else of 256 rows where rows
+// and tokens give every SM a block, of 128 over two streams otherwise, with splits of
+// at least two tiles per stream up to one block per SM.
 //
 // Warp-level kernels: blocks of up to 32 rows.  Wide blocks take long rows where one
 // block each fills the SMs once (104 to 148; batch 16 at 64K, window 8192: 88 us, 94
@@ -999,7 +1005,8 @@ DensePlan dense_plan(int units, int group, int n_q, int d, long long tokens, int
   if (out_bf16 && rows >= kTensorRows) {
     const long long tiles = (tokens + 127) / 128, wide = (long long)units * ((rows + 255) / 256);
     f.tensor = 1;
-    f.row_block = rows > 128 && wide * (tiles / 2 > 1 ? tiles / 2 : 1) >= kNumSMs ? 256 : 128;
+    f.solo = units * ((rows + 127) / 128) >= kSlots && tiles <= solo_tiles(d);
+    f.row_block = !f.solo && rows > 128 && wide * (tiles / 2 > 1 ? tiles / 2 : 1) >= kNumSMs ? 256 : 128;
     f.blocks = (int)((rows + f.row_block - 1) / f.row_block);
     const long long ctas = (long long)units * f.blocks, most = tiles / (f.row_block == 256 ? 2 : 4);
     long long s = kNumSMs / ctas;

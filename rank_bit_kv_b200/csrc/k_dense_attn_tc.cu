@@ -9,15 +9,17 @@
 // at d = 128) and 128^2 exponentials (1024 clocks at 16 a clock).  So two score
 // tiles ("streams") are in flight per CTA, and while the softmax of one runs on
 // its four warps the tensor core works on the other:
-//   warps 0-3, 4-7   softmax of stream 0 / 1, one thread per row: scores from TMEM,
+//   warps 0-3, 4-7   (kSolo: 0-3, 4, 5) softmax of stream 0 / 1, one thread per row: scores from TMEM,
 //                    mask, maximum, exponentials, P back into TMEM over the scores
 //   warp 8           issues the MMAs: S = Q K^T from shared memory, O += P V with P
 //                    from TMEM (one warp per stream: 427 us for the prefill of 8192
 //                    tokens that took 335 so; interleaved MMAs of two warps run slower)
 //   warp 9           loads 128-token tiles of K and V by TMA into a ring
-// PAIR: the streams are two tiles of 128 query rows and share the K/V tiles.
-// Otherwise (up to 128 rows, or too few blocks to fill the SMs) they are the
-// same 128 rows over the even and the odd tiles, merged through shared memory.
+// kPair: the streams are two tiles of 128 query rows and share the K/V tiles.
+// kSplit (up to 128 rows, or too few blocks to fill the SMs): they are the same 128 rows
+// over the even and the odd tiles, merged through shared memory.
+// kSolo (many blocks of few tiles): one stream per CTA, two CTAs per SM, so that one's
+// first loads and last stores run beside the other's tiles.
 //
 // A prompt of 8192 tokens, window 2048, 32/8 heads of 128: 272 us, 885 TFLOP/s of what its
 // queries see.  What is left is a stream's chain of softmax, P V and Q K^T, which two
@@ -40,24 +42,24 @@ using namespace tc;
 
 constexpr int kTM = 128;                 // query rows per stream
 constexpr int kTN = 128;                 // tokens per tile
-constexpr int kWarpMma = 8, kWarpTma = 9;
-constexpr int kThreads = 320;
-constexpr int kSoftThreads = 256;
+enum Kind { kPair = 0, kSplit = 1, kSolo = 2 };
 constexpr float kSlack = 24.f;           // how far scores may pass the reference maximum (log2)
 
-template <int D>
+template <int D, int KIND>
 struct Cfg {
+  static constexpr int kStreams = KIND == kSolo ? 1 : 2;
+  static constexpr int kSoftThreads = kTM * kStreams;    // one per row of a stream
+  static constexpr int kThreads = kSoftThreads + 64;
   static constexpr int kHalfB = kTN * 128;               // 64 elements of 128 rows, 128-byte swizzle
   static constexpr int kTileB = kHalfB * (D / 64);       // a K, V or Q tile
-  static constexpr int kStages = D == 128 ? 5 : 10;
-  static constexpr int kSmem = (2 + kStages) * kTileB + 1024;
+  static constexpr int kTilesQ = KIND == kPair ? 2 : 1;
+  static constexpr int kStages = (KIND == kSolo ? 2 : KIND == kPair ? 5 : 6) * (128 / D);
+  static constexpr int kSmem = (kTilesQ + kStages) * kTileB + 1024;
+  // TMEM columns: the scores of the streams (P over them), then their outputs
+  static constexpr uint32_t kTmemCols = kStreams * 256;
+  static __device__ __forceinline__ uint32_t col_s(int s) { return (uint32_t)s * kTN; }
+  static __device__ __forceinline__ uint32_t col_o(int s) { return kStreams * kTN + (uint32_t)s * D; }
 };
-
-// TMEM columns: the scores of both streams (P over them), then their outputs.
-constexpr uint32_t kTmemCols = 512;
-__device__ __forceinline__ uint32_t col_s(int s) { return (uint32_t)s * kTN; }
-template <int D>
-__device__ __forceinline__ uint32_t col_o(int s) { return 2 * kTN + (uint32_t)s * D; }
 
 constexpr uint32_t idesc_bf16(int n, int b_mn_major) {
   return idesc_f16(kTM, n, 0, b_mn_major) | (1u << 7) | (1u << 10);      // A and B are bf16
@@ -157,9 +159,9 @@ __device__ __forceinline__ uint32_t pack_bf2(float2 x) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int D>
+template <int STAGES>
 struct __align__(8) Bars {
-  uint64_t q_full, full[Cfg<D>::kStages], empty[Cfg<D>::kStages];
+  uint64_t q_full, full[STAGES], empty[STAGES];
   uint64_t s_full[2], p_full[2][2], o_done[2], drain;       // p_full: [stream][half of the tokens]
   uint32_t tmem;
   int abort;
@@ -178,25 +180,30 @@ struct Tiles {
 };
 
 // Ring position of K tile t and V tile t of n: K runs `lead` tiles ahead of V
-// (K0, V0, K1, V1 ... or K0, K1, V0, K2, V1 ...).
-template <bool PAIR>
-__device__ __forceinline__ int ring_k(int t) { return PAIR ? 2 * t : (t < 2 ? t : 2 * t - 1); }
-template <bool PAIR>
-__device__ __forceinline__ int ring_v(int t, int n) { return PAIR ? 2 * t + 1 : min(2 * t + 2, 2 * n - 1); }
+// (K0, V0, K1, V1 ..., or K0, K1, V0, K2, V1 ... where the streams alternate).
+template <int KIND>
+struct Ring {
+  static constexpr int lead = KIND == kSplit ? 2 : 1;
+  static __device__ __forceinline__ int k(int t) { return KIND != kSplit ? 2 * t : (t < 2 ? t : 2 * t - 1); }
+  static __device__ __forceinline__ int v(int t, int n) { return KIND != kSplit ? 2 * t + 1 : min(2 * t + 2, 2 * n - 1); }
+};
 
-template <int D, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int KIND>
+__global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, KIND == kSolo ? 2 : 1)
     dense_attn_tc_kernel(const __grid_constant__ DenseAttn p, const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v) {
-  using C = Cfg<D>;
-  constexpr int RB = PAIR ? 2 * kTM : kTM;
+  using C = Cfg<D, KIND>;
+  using R = Ring<KIND>;
+  constexpr bool PAIR = KIND == kPair, SPLIT = KIND == kSplit;
+  constexpr int RB = PAIR ? 2 * kTM : kTM, kSoftThreads = C::kSoftThreads;
+  constexpr int kWarpMma = kSoftThreads / 32, kWarpTma = kWarpMma + 1;
   constexpr int NST = C::kStages;
   extern __shared__ uint8_t dsm_raw[];
-  __shared__ Bars<D> bars;
+  __shared__ Bars<NST> bars;
   // swizzled tiles start on 1024-byte boundaries
   uint8_t* const dsm = dsm_raw + ((1024u - (smem_u32(dsm_raw) & 1023u)) & 1023u);
   uint8_t* const sm_q = dsm;
-  uint8_t* const ring = dsm + 2 * C::kTileB;
+  uint8_t* const ring = dsm + C::kTilesQ * C::kTileB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % p.own.splits, ub = blockIdx.x / p.own.splits;
   const int u = ub / p.own.blocks, r0 = (ub % p.own.blocks) * RB;
@@ -223,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kWarpMma) {
     // queries: a warp its rows, neighbouring lanes the chunks of one (a row per lane
     // takes 4000 clocks more of the copies' issue); zero past the block's rows
-    constexpr int RPW = RB / 8, CPR = D / 8, RPI = 32 / CPR;
+    constexpr int RPW = RB / kWarpMma, CPR = D / 8, RPI = 32 / CPR;
     const int mine = warp * RPW + lane % RPW;
     const long long off = dense_row_at(p, u, r0 + min(mine, n_rows - 1));
 #pragma unroll
@@ -248,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
-    tmem_alloc(&bars.tmem, kTmemCols);
+    tmem_alloc(&bars.tmem, C::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++pos;
         issued = pos;
       };
-      constexpr int lead = PAIR ? 1 : 2;
+      constexpr int lead = R::lead;
       for (int t = 0; t < lead && t < n && ok; ++t) load(&map_k, t);
       for (int t = 0; t < n && ok; ++t) {
         load(&map_v, t);
@@ -314,9 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto qk = [&](int s, int t) {
         int t0, nt;
         tu.at(t, t0, nt);
-        const uint32_t id = idesc_bf16((nt + 15) & ~15, 0), sd = tmem + col_s(s);
+        const uint32_t id = idesc_bf16((nt + 15) & ~15, 0), sd = tmem + C::col_s(s);
         const uint64_t qd = desc_sw128(qa + (PAIR ? s * C::kTileB : 0), 0, 1024);
-        const uint64_t kd = desc_sw128(ring0 + ring_k<PAIR>(t) % NST * C::kTileB, 0, 1024);
+        const uint64_t kd = desc_sw128(ring0 + R::k(t) % NST * C::kTileB, 0, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk / 4) * C::kHalfB + (kk % 4) * 32) >> 4;
@@ -325,11 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto full = [&](int pos) { wait(&bars.full[pos % NST], (pos / NST) & 1); };
       auto release = [&](int pos) { commit_lead(lead, &bars.empty[pos % NST]); };
-      constexpr int hop = PAIR ? 1 : 2;                  // a stream's tiles are t, t + hop, ...
+      constexpr int hop = R::lead;                  // a stream's tiles are t, t + hop, ...
       // stream s: O over V tile t (its j-th), and S over the next K tile, issued in one
       // go; first, last: it is the first or last stream to use these tiles
       auto step = [&](int s, int j, int t, bool first, bool last) {
-        const int pos_v = ring_v<PAIR>(t, n), pos_k = ring_k<PAIR>(t + hop);
+        const int pos_v = R::v(t, n), pos_k = R::k(t + hop);
         const bool next = t + hop < n;
         int t0, nt;
         tu.at(t, t0, nt);
@@ -351,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         constexpr uint32_t id = idesc_bf16(D, 1);
         const uint64_t vd = desc_sw128(ring0 + pos_v % NST * C::kTileB, C::kHalfB, 1024);
-        const uint32_t sd = tmem + col_s(s), od = tmem + col_o<D>(s);
+        const uint32_t sd = tmem + C::col_s(s), od = tmem + C::col_o(s);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           wait(&bars.p_full[s][h], j & 1);
@@ -377,26 +384,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (next) release(pos_k);
         }
       };
-      full(ring_k<PAIR>(0));
+      full(R::k(0));
       if (ok) {
         qk(0, 0);
         commit_lead(lead, &bars.s_full[0]);
         if (!PAIR) release(0);
       }
-      if (PAIR || n > 1) {
-        if (!PAIR) full(ring_k<PAIR>(1));
+      if (PAIR || (SPLIT && n > 1)) {
+        if (SPLIT) full(R::k(1));
         if (ok) {
           qk(1, PAIR ? 0 : 1);
           commit_lead(lead, &bars.s_full[1]);
-          release(PAIR ? 0 : ring_k<PAIR>(1));
+          release(PAIR ? 0 : R::k(1));
         }
       }
       for (int t = 0; t < n && ok; ++t) {
         if (PAIR) {
           step(0, t, t, true, false);
           step(1, t, t, false, true);
-        } else {
+        } else if (SPLIT) {
           step(t & 1, t >> 1, t, true, true);
+        } else {
+          step(0, t, t, true, true);
         }
       }
       if (!ok && lane == 0) {
@@ -421,19 +430,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // positions of the stream's rows
     const int s_lo = PAIR ? dense_row_pos(p, len, r0 + min(s * kTM, n_rows - 1)) : p_lo;
     const int s_hi = PAIR ? dense_row_pos(p, len, r0 + min(s * kTM + kTM, n_rows) - 1) : p_hi;
-    const int n_s = PAIR ? n : (n + 1 - s) / 2;
+    const int n_s = SPLIT ? (n + 1 - s) / 2 : n;
     const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
     float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n_s; ++j) {
       int t0, nt;
-      tl.at(PAIR ? j : 2 * j + s, t0, nt);
+      tl.at(SPLIT ? 2 * j + s : j, t0, nt);
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[s], j & 1, abort, err)))) break;
       tc_fence_after();
       uint32_t x[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        tmem_ld32(tl_base + col_s(s) + 32 * c, x[c]);
+        tmem_ld32(tl_base + C::col_s(s) + 32 * c, x[c]);
       tmem_wait_ld();
 #pragma unroll
       for (int c = 0; c < 4; ++c) reg_fence(x[c]);
@@ -480,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[i & 1] = add2(sum[i & 1], v);
             w[i] = pack_bf2(v);
           }
-          tmem_st16(tl_base + col_s(s) + 16 * c, w);
+          tmem_st16(tl_base + C::col_s(s) + 16 * c, w);
         }
       };
       auto arrive = [&](int h) {                         // one arrival per warp: they are taken one by one
@@ -518,12 +527,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               uint32_t o[16];
-              tmem_ld16(tl_base + col_o<D>(s) + c, o);
+              tmem_ld16(tl_base + C::col_o(s) + c, o);
               tmem_wait_ld();
               reg_fence(o);
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-              tmem_st16(tl_base + col_o<D>(s) + c, o);
+              tmem_st16(tl_base + C::col_o(s) + c, o);
             }
           }
         }
@@ -539,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && n_s > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_done[s], (n_s - 1) & 1, abort, err));
     tc_fence_after();
     float* const stage = reinterpret_cast<float*>(ring);  // [D][kTM]: the ring's loads are over
-    if (!PAIR) {
+    if (SPLIT) {
       if (s == 1) {
         bars.ml[row][0] = m_ref;
         bars.ml[row][1] = l;
@@ -549,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             uint32_t o[16];
-            tmem_ld16(tl_base + col_o<D>(s) + c, o);
+            tmem_ld16(tl_base + C::col_o(s) + c, o);
             tmem_wait_ld();
             reg_fence(o);
 #pragma unroll
@@ -559,12 +568,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       named_bar(1, kSoftThreads);
     }
-    if ((PAIR || s == 0) && r - (r & 31) < n_rows) {
+    if ((!SPLIT || s == 0) && r - (r & 31) < n_rows) {
       float a0 = 1.f, a1 = 0.f;
       // a stream that saw nothing adds nothing
       const bool mine = !(m_ref == -INFINITY && l == 0.f);
       bool other = false;
-      if (!PAIR) {
+      if (SPLIT) {
         const float m1 = bars.ml[row][0], l1 = bars.ml[row][1];
         other = n > 1 && !(m1 == -INFINITY && l1 == 0.f);
         if (other) {
@@ -588,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto values = [&](int c, float (&f)[16]) {
         uint32_t o[16];
-        tmem_ld16(tl_base + col_o<D>(s) + c, o);
+        tmem_ld16(tl_base + C::col_o(s) + c, o);
         tmem_wait_ld();
         reg_fence(o);
 #pragma unroll
@@ -663,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == kWarpMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
@@ -689,25 +698,30 @@ cudaError_t tensor_map(CUtensorMap* map, const DenseAttn& p, const __nv_bfloat16
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, bool PAIR>
+template <int D, int KIND>
 cudaError_t launch(const DenseAttn& p, cudaStream_t s) {
+  using C = Cfg<D, KIND>;
   CUtensorMap mk, mv;
   cudaError_t e = tensor_map(&mk, p, p.k);
   if (e == cudaSuccess) e = tensor_map(&mv, p, p.v);
   if (e != cudaSuccess) return e;
-  auto* f = dense_attn_tc_kernel<D, PAIR>;
-  e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  auto* f = dense_attn_tc_kernel<D, KIND>;
+  e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  f<<<(unsigned)((long long)p.units * p.own.blocks * p.own.splits), kThreads, Cfg<D>::kSmem, s>>>(p, mk, mv);
+  f<<<(unsigned)((long long)p.units * p.own.blocks * p.own.splits), C::kThreads, C::kSmem, s>>>(p, mk, mv);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_kind(const DenseAttn& p, cudaStream_t s) {
+  if (p.own.row_block == 2 * kTM) return launch<D, kPair>(p, s);
+  return p.solo ? launch<D, kSolo>(p, s) : launch<D, kSplit>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_dense_attn_tc(const DenseAttn& p, cudaStream_t s) {
-  const bool pair = p.own.row_block == 2 * kTM;
-  if (p.d == 128) return pair ? launch<128, true>(p, s) : launch<128, false>(p, s);
-  return pair ? launch<64, true>(p, s) : launch<64, false>(p, s);
+  return p.d == 128 ? launch_kind<128>(p, s) : launch_kind<64>(p, s);
 }
 
 }  // namespace kvc

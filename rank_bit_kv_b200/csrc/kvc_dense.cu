@@ -95,6 +95,7 @@ char* take_plan(kvc::DenseAttn* p, const kvc::DensePlan& f, bool partials, char*
   p->own.row_block = f.row_block;
   p->own.blocks = f.blocks;
   p->own.splits = f.splits;
+  p->solo = f.solo;
   p->wide = f.wide;
   p->no_copies = kvc::test_no_copies();
   p->own.flat = f.flat;

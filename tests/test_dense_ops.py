@@ -1003,3 +1003,35 @@ def test_bounded_waits_give_up_report_and_leave_the_context_usable(n_q, Hq):
     assert int(ws[:4].view(torch.int32)) == 0
     ref, tol = D.window_attention(_f64(q)[:, :1], _f64(p.k)[:, :1], _f64(p.v)[:, :1], p.lens, 400, 4, p.scale, True, 8)
     within(_f64(out)[:, :1], ref, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,T,n_q,W,S,G,bad", [(128, 200, 70, 33, 5, 4, False), (64, 200, 70, 200, 0, 4, True),
+                                               (128, 700, 65, 130, 40, 4, False), (128, 90, 90, 90, 0, 3, True),
+                                               (64, 1500, 130, 500, 64, 2, False)])
+def test_window_many_blocks_of_few_tiles(d, T, n_q, W, S, G, bad):
+    """Enough row blocks to fill the SMs twice, with few tokens each."""
+    import torch
+
+    B, Hkv = 19, 8
+    lens = [T, 0, 1, T - 1, n_q, n_q - 1, T // 2] + [T - 3 * i for i in range(B - 7)]
+    p = Problem(B, Hkv * G, Hkv, d, T, lens, cap=T + 3, bf16=1, seed=90)
+    if bad:
+        p.v[0, 2, T - 20, 1] = float("nan")                  # seen by some queries of its row only
+    q, out = p.queries(n_q, gain=1.5)
+    p.window(q, out, W, S)
+    v = p.v.clone()
+    if bad:
+        v[0, 2, T - 20, 1] = 0
+    for b, n in enumerate(lens):
+        pos = torch.arange(n - n_q, n, device="cuda")[:, None]
+        t = torch.arange(n, device="cuda")
+        seen = (t <= pos) & ((t < S) | (t > pos - W))
+        for h in range(0, Hkv * G, 3 if b else 1):
+            ref, tol, _ = _on_gpu(q[b, h], p.k[b, h // G, :n], v[b, h // G, :n], seen, p.scale, True)
+            got = _f64(out[b, h])
+            if bad and b == 0 and h // G == 2:
+                hit = seen[:, T - 20].cpu().numpy()
+                assert hit.any() and not hit.all() and np.isnan(got[hit, 1]).all()
+                got, ref, tol = got[~hit], ref[~hit], tol[~hit]
+            within(got, ref, tol, f"row {b} head {h}")
