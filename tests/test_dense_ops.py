@@ -1035,3 +1035,70 @@ def test_window_many_blocks_of_few_tiles(d, T, n_q, W, S, G, bad):
                 assert hit.any() and not hit.all() and np.isnan(got[hit, 1]).all()
                 got, ref, tol = got[~hit], ref[~hit], tol[~hit]
             within(got, ref, tol, f"row {b} head {h}")
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits_in_the_other_kernels():
+    """The tcgen05 kernel, the weighted decode, the shared prefix and the eviction on a late unit of a
+    cache whose element offsets pass 2^32, against a small cache of the same tokens."""
+    import torch
+
+    B, Hkv, T, d, n = 2, 9, 1 << 21, 128, 3000               # 18 units of 2^28 elements
+    big = dense(B, Hkv, Hkv, d, T, bf16=1)
+    cache = kvc.Cache(big)                                   # zeros
+    small = Problem(1, 1, 1, d, n, bf16=1, seed=41)
+    kv = {name: cache.bufs[name].view(torch.bfloat16).view(B, Hkv, T, d) for name in ("k_dense", "v_dense")}
+    kv["k_dense"][1, 8, :n], kv["v_dense"][1, 8, :n] = small.k[0, 0], small.v[0, 0]
+    cache.seq_lens = torch.tensor([1, n], dtype=torch.int32, device="cuda")
+    cache.n_tokens = n
+    close = lambda a, b: ((a.double() - b.double()).abs() <= 2.0**-7 * b.double().abs() + 1e-4).all()  # noqa: E731
+    # prefill rows on tcgen05: the same scores in another split, one step of bf16 apart at most
+    q1, o1 = small.queries(200)
+    small.window(q1, o1, 1000, 4)
+    q = torch.zeros(B, Hkv, 200, d, dtype=torch.bfloat16, device="cuda")
+    q[1, 8] = q1[0, 0]
+    out = torch.empty_like(q)
+    ws = torch.empty(max(big.window_workspace_bytes(n, 200), big.accum_workspace_bytes(n),
+                         big.prefix_workspace_bytes(n, 100)), dtype=torch.uint8, device="cuda")
+    kvc.window_attn(big, cache, q, out, ws, 1000, 4)
+    assert close(out[1, 8], o1[0, 0])
+    # one token with weights, and behind a prefix
+    qa, oa = small.queries()
+    w1 = torch.zeros(1, 1, n, device="cuda")
+    kvc.decode_accum(small.layout, small.cache, qa, w1, oa, small.ws(small.layout.accum_workspace_bytes(n)))
+    q = torch.zeros(B, Hkv, d, dtype=torch.bfloat16, device="cuda")
+    q[1, 8] = qa[0, 0]
+    out = torch.empty_like(q)
+    w = torch.zeros(B, Hkv, T, device="cuda")
+    kvc.decode_accum(big, cache, q, w, out, ws)
+    assert close(out[1, 8], oa[0, 0])
+    assert ((w[1, 8, :n] - w1[0, 0]).abs() <= 1e-5 * w1[0, 0]).all() and (w[1, 8, n:] == 0).all()
+    pre = Problem(1, Hkv, Hkv, d, 100, seed=42)
+    kvc.prefix_decode(pre.layout, pre.cache, big, cache, q, out, ws)
+    ref, tol = D.prefix_attention(_f64(q)[1:, 8:], _f64(pre.k)[0, 8:], _f64(pre.v)[0, 8:], _f64(small.k), _f64(small.v),
+                                  [n], d**-0.5, True, 8)
+    within(_f64(out)[1:, 8:], ref, tol)
+    # eviction in place
+    w[1, 8, :n] = torch.rand(n, generator=small.gen, device="cuda")
+    w0 = w[1, 8, :n].clone()
+    kept, lens = kvc.evict(big, cache, big, cache, w, w, 700, 4, 50)
+    assert lens.tolist() == [1, 700]
+    want = D.evict(w0[None, None].cpu().numpy(), [n], 700, 4, 50)[0]
+    assert kept[1, 8].tolist() == want
+    at = torch.tensor(want, device="cuda")
+    for name, src in (("k_dense", small.k), ("v_dense", small.v)):
+        assert torch.equal(kv[name][1, 8, :700], src[0, 0][at])
+    assert torch.equal(w[1, 8, :700], w0[at]) and (w[1, 8, 700:] == 0).all()
+
+
+@pytest.mark.gpu
+def test_evict_of_an_empty_cache():
+    import torch
+
+    p = Problem(2, 2, 2, 64, 50, cap=60, seed=43)
+    p.cache.n_tokens = 0
+    w, w2 = torch.ones(2, 2, 60, device="cuda"), torch.ones(2, 2, 40, device="cuda")
+    o = Problem(2, 2, 2, 64, 40, seed=44)
+    k1 = o.k.clone()
+    kept, lens = kvc.evict(p.layout, p.cache, o.layout, o.cache, w, w2, 32, 4, 8)
+    assert (kept == -1).all() and lens.tolist() == [0, 0] and (w2 == 0).all() and torch.equal(o.k, k1)
