@@ -1,4 +1,5 @@
-"""Build libkvc.so in-tree with nvcc for sm_100a (B200).
+"""Build libkvc.so in-tree with nvcc for sm_100a (B200), and the Python binding of
+its serving operators (_serving.so) with g++.
 
     python -m rank_bit_kv_b200.build        # incremental
     python -m rank_bit_kv_b200.build --force
@@ -17,6 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkvc.so")
+BINDING = os.path.join(HERE, "_serving.so")
+BINDING_SRC = os.path.join(CSRC, "serving_binding.cpp")
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -49,6 +52,24 @@ def _compile(src, extra):
     return obj, r.stderr
 
 
+def _build_binding():
+    """_serving.so: against torch's headers and libkvc.so beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = [*cpp_extension.include_paths("cuda"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DTORCH_EXTENSION_NAME=_serving",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{p}" for p in inc), BINDING_SRC, "-o", BINDING,
+           *(f"-L{p}" for p in cpp_extension.library_paths("cuda")), "-lc10", "-lc10_cuda", "-ltorch",
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", f"-L{HERE}", "-l:libkvc.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+
+
 def build(force=False, verbose=False, extra=()):
     """Compile every kernel source and link libkvc.so.  Returns the library path."""
     os.makedirs(OBJ, exist_ok=True)
@@ -66,6 +87,8 @@ def build(force=False, verbose=False, extra=()):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    if force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "kvc.h")]):
+        _build_binding()
     return LIB
 
 

@@ -1,0 +1,163 @@
+// Python binding of the serving operators on dense layouts: the checks of the
+// tensors that the C ABI cannot make, the current stream, and the call.  These
+// operators are called once per token and layer, where the checks in Python
+// and the call through ctypes took longer (6 us) than the smallest kernels.
+#include <ATen/cuda/CUDAContextLight.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/extension.h>
+
+#include <string>
+
+#include "../../include/kvc.h"
+
+namespace {
+
+using at::Tensor;
+using OptTensor = std::optional<Tensor>;
+
+[[noreturn]] void refuse(const std::string& what) { throw py::value_error(what); }
+
+// A dense layout: its handle and what the checks need of it.
+struct Dense {
+  uintptr_t handle;
+  int64_t layers, batch, q_heads, kv_heads, head_dim, capacity, bytes;
+  bool bf16;
+  const kvc_layout* get() const { return reinterpret_cast<const kvc_layout*>(handle); }
+  at::ScalarType out_type() const { return bf16 ? at::kBFloat16 : at::kFloat; }
+};
+
+// A shape: [n_layers,] then the given extents (the layer axis where a call covers all layers).
+struct Shape {
+  int64_t n[5];
+  int64_t dims = 0;
+  Shape(const Dense& L, int64_t layer, std::initializer_list<int64_t> rest) {
+    if (L.layers > 1 && layer == 0) n[dims++] = L.layers;
+    for (int64_t x : rest) n[dims++] = x;
+  }
+  at::IntArrayRef ref() const { return at::IntArrayRef(n, dims); }
+};
+
+void* tensor(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape, c10::Device device) {
+  if (t.scalar_type() != type || t.sizes() != shape || t.device() != device || !t.is_contiguous()) {
+    std::ostringstream s;
+    s << name << " must be a contiguous " << type << " tensor of shape " << shape << " on " << device << ", got "
+      << t.scalar_type() << " " << t.sizes() << " on " << t.device() << (t.is_contiguous() ? "" : ", not contiguous");
+    refuse(s.str());
+  }
+  return t.data_ptr();
+}
+
+kvc_cache cache(const Dense& L, const Tensor& k, const Tensor& v, const OptTensor& lens, int64_t n_tokens,
+                int64_t layer, c10::Device device) {
+  kvc_cache c = {};
+  for (const Tensor* t : {&k, &v})
+    if (t->device() != device || (int64_t)t->nbytes() < L.bytes || !t->is_contiguous()) {
+      std::ostringstream s;
+      s << "cache.k_dense and v_dense must be contiguous buffers of " << L.bytes << " bytes on " << device;
+      refuse(s.str());
+    }
+  c.k_dense = k.data_ptr();
+  c.v_dense = v.data_ptr();
+  if (lens) c.seq_lens = static_cast<int32_t*>(tensor(*lens, "cache.seq_lens", at::kInt, {L.batch}, device));
+  if (n_tokens != (int32_t)n_tokens || layer != (int32_t)layer) refuse("cache.n_tokens or layer is out of range");
+  c.n_tokens = (int32_t)n_tokens;
+  c.layer = (int32_t)layer;
+  return c;
+}
+
+// The device made current, and the stream of the call: torch's current one unless given.
+struct Call {
+  c10::cuda::OptionalCUDAGuard guard;
+  void* stream;
+  Call(c10::Device device, const std::optional<uintptr_t>& given) {
+    if (!device.is_cuda()) refuse("the tensors are on " + device.str() + ", not on a GPU");
+    guard.set_device(device);
+    stream = given ? reinterpret_cast<void*>(*given)
+                   : static_cast<void*>(c10::cuda::getCurrentCUDAStream(device.index()).stream());
+  }
+};
+
+void workspace(const Tensor& ws, c10::Device device) {
+  if (ws.device() != device || !ws.is_contiguous()) refuse("ws must be a contiguous buffer on " + device.str());
+}
+
+int window_attn(const Dense& L, const Tensor& k, const Tensor& v, const OptTensor& lens, int64_t n_tokens,
+                int64_t layer, const Tensor& q, const Tensor& out, const Tensor& ws, int32_t window, int32_t sinks,
+                const std::optional<uintptr_t>& stream) {
+  const auto dev = q.device();
+  if (q.dim() != 4 + (L.layers > 1 && layer == 0))
+    refuse("q must be [B, Hq, n_q, d] (all layers at once: [n_layers, B, Hq, n_q, d])");
+  const int64_t n_q = q.size(-2);
+  if (n_q != (int32_t)n_q) refuse("q has too many tokens");
+  const Shape shape(L, layer, {L.batch, L.q_heads, n_q, L.head_dim});
+  const void* qp = tensor(q, "q", at::kBFloat16, shape.ref(), dev);
+  void* op = tensor(out, "out", L.out_type(), shape.ref(), dev);
+  const kvc_cache c = cache(L, k, v, lens, n_tokens, layer, dev);
+  workspace(ws, dev);
+  const Call call(dev, stream);
+  return kvc_window_attn(L.get(), &c, qp, (int32_t)n_q, window, sinks, op, ws.data_ptr(), ws.nbytes(), call.stream);
+}
+
+int decode_accum(const Dense& L, const Tensor& k, const Tensor& v, const OptTensor& lens, int64_t n_tokens,
+                 int64_t layer, const Tensor& q, const Tensor& weights, const Tensor& out, const Tensor& ws,
+                 const std::optional<uintptr_t>& stream) {
+  const auto dev = q.device();
+  const Shape shape(L, layer, {L.batch, L.q_heads, L.head_dim});
+  const void* qp = tensor(q, "q", at::kBFloat16, shape.ref(), dev);
+  void* op = tensor(out, "out", L.out_type(), shape.ref(), dev);
+  void* wp = tensor(weights, "weights", at::kFloat, Shape(L, layer, {L.batch, L.kv_heads, L.capacity}).ref(), dev);
+  const kvc_cache c = cache(L, k, v, lens, n_tokens, layer, dev);
+  workspace(ws, dev);
+  const Call call(dev, stream);
+  return kvc_decode_accum(L.get(), &c, qp, static_cast<float*>(wp), op, ws.data_ptr(), ws.nbytes(), call.stream);
+}
+
+py::tuple evict(const Dense& L, const Tensor& k, const Tensor& v, const OptTensor& lens, int64_t n_tokens,
+                int64_t layer, const Dense& L2, const Tensor& k2, const Tensor& v2, int64_t layer2,
+                const Tensor& weights, const Tensor& weights2, int32_t keep, int32_t sinks, int32_t recent,
+                const std::optional<uintptr_t>& stream) {
+  const auto dev = weights.device();
+  void* wp = tensor(weights, "weights", at::kFloat, Shape(L, layer, {L.batch, L.kv_heads, L.capacity}).ref(), dev);
+  void* wp2 = tensor(weights2, "dst_weights", at::kFloat, Shape(L2, layer2, {L2.batch, L2.kv_heads, L2.capacity}).ref(),
+                     dev);
+  const kvc_cache a = cache(L, k, v, lens, n_tokens, layer, dev);
+  const kvc_cache b = cache(L2, k2, v2, std::nullopt, 0, layer2, dev);
+  const Call call(dev, stream);
+  const auto ints = weights.options().dtype(at::kInt);
+  Tensor kept = at::empty(Shape(L, layer, {L.batch, L.kv_heads, keep > 0 ? keep : 0}).ref(), ints);
+  Tensor new_lens = at::empty({L.batch}, ints);
+  const int st = kvc_evict(L.get(), &a, L2.get(), &b, static_cast<float*>(wp), static_cast<float*>(wp2), keep, sinks,
+                           recent, static_cast<int32_t*>(kept.data_ptr()), static_cast<int32_t*>(new_lens.data_ptr()),
+                           call.stream);
+  return py::make_tuple(st, std::move(kept), std::move(new_lens));
+}
+
+int prefix_decode(const Dense& P, const Tensor& pk, const Tensor& pv, const OptTensor& plens, int64_t pn,
+                  int64_t player, const Dense& L, const Tensor& k, const Tensor& v, const OptTensor& lens,
+                  int64_t n_tokens, int64_t layer, const Tensor& q, const Tensor& out, const Tensor& ws,
+                  const std::optional<uintptr_t>& stream) {
+  const auto dev = q.device();
+  const Shape shape(L, layer, {L.batch, L.q_heads, L.head_dim});
+  const void* qp = tensor(q, "q", at::kBFloat16, shape.ref(), dev);
+  void* op = tensor(out, "out", L.out_type(), shape.ref(), dev);
+  const kvc_cache a = cache(P, pk, pv, plens, pn, player, dev);
+  const kvc_cache b = cache(L, k, v, lens, n_tokens, layer, dev);
+  workspace(ws, dev);
+  const Call call(dev, stream);
+  return kvc_prefix_decode(P.get(), &a, L.get(), &b, qp, op, ws.data_ptr(), ws.nbytes(), call.stream);
+}
+
+}  // namespace
+
+PYBIND11_MODULE(_serving, m) {
+  py::class_<Dense>(m, "Dense")
+      .def(py::init([](uintptr_t handle, int64_t layers, int64_t batch, int64_t q_heads, int64_t kv_heads,
+                       int64_t head_dim, int64_t capacity, int64_t bytes, bool bf16) {
+        return Dense{handle, layers, batch, q_heads, kv_heads, head_dim, capacity, bytes, bf16};
+      }));
+  m.def("window_attn", &window_attn);
+  m.def("decode_accum", &decode_accum);
+  m.def("evict", &evict);
+  m.def("prefix_decode", &prefix_decode);
+}

@@ -194,17 +194,25 @@ class Layout:
         check(lib().kvc_create_layout(C.byref(desc), C.byref(h)))
         self.h = h
         self.desc = desc
-        # (layers, batch, query heads, KV heads, head dim, max_tokens, bf16 output) of a dense layout
-        self._dense = None
+        # what the serving operators' binding checks of a dense layout (as the handle was created)
+        self._dense_args = self._dense = None
         if desc.kind == KVC_DENSE_BF16:
-            self._dense = (max(1, desc.n_layers), desc.batch, desc.n_q_heads, desc.n_kv_heads, desc.head_dim,
-                           desc.max_tokens, bool(desc.out_bf16))
-            self._dense_bytes = self.buffer_sizes()["k_dense"]
+            self._dense_args = (h.value, max(1, desc.n_layers), desc.batch, desc.n_q_heads, desc.n_kv_heads,
+                                desc.head_dim, desc.max_tokens, self.buffer_sizes()["k_dense"],
+                                bool(desc.out_bf16))
 
     def __del__(self):
         if getattr(self, "h", None) and _lib is not None:
             _lib.kvc_destroy_layout(self.h)
             self.h = None
+
+    def dense(self):
+        """The layout as the serving operators' binding takes it; ValueError unless it is dense."""
+        if self._dense is None:
+            if self._dense_args is None:
+                raise ValueError("the serving operators take dense layouts")
+            self._dense = _serving().Dense(*self._dense_args)
+        return self._dense
 
     def buffer_sizes(self):
         arr = (C.c_size_t * NBUF)()
@@ -508,69 +516,33 @@ def block_compact(src_layout, src_cache, dst_layout, dst_cache, kept, stream=Non
 
 # --------------------------------------------------------------------------- serving operators
 #
-# On dense bf16 layouts.  Tensors are contiguous and on one device; a call whose
+# On dense bf16 layouts, through _serving.so (csrc/serving_binding.cpp), which checks
+# the tensors: contiguous, of the layout's shapes and types, on one GPU.  A call whose
 # tensors are not on the current device makes theirs current for its duration.
 # `stream` is a cudaStream_t (default: torch's current stream of that device).
 
-
-def _tensor(t, name, dtype, shape, device):
-    """t's address, after the checks that the C ABI cannot make."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+_ext = None
 
 
-def _run(device, stream, call, *args):
-    """call(*args, stream) with `device` current; raises what the library reports."""
-    import torch
+def _serving():
+    """The binding (raises if it is missing: there is no other path)."""
+    global _ext
+    if _ext is None:
+        import torch  # noqa: F401  (its libraries are loaded before the binding's)
 
-    if device.type != "cuda":
-        raise ValueError(f"the tensors are on {device}, not on a GPU")
-    index = device.index
-    if index != torch._C._cuda_getDevice():
-        with torch.cuda.device(device):
-            return _run(device, stream, call, *args)
-    status = call(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+        lib()
+        from rank_bit_kv_b200 import _serving as ext
+        _ext = ext
+    return _ext
+
+
+def _stream(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.value or 0
+
+
+def _checked(status):
     if status:
         check(status)
-
-
-def _dense_dims(layout, cache):
-    """(leading layer axis, batch, query heads, KV heads, head dim, capacity, output type) of a dense call."""
-    import torch
-
-    if layout._dense is None:
-        raise ValueError("the serving operators take dense layouts")
-    layers, B, Hq, Hkv, d, cap, bf16 = layout._dense
-    return ((layers,) if layers > 1 and not cache.layer else (), B, Hq, Hkv, d, cap,
-            torch.bfloat16 if bf16 else torch.float32)
-
-
-def _dense_cache(layout, cache, device, batch):
-    """The cache's C struct, after checks of its buffers against the layout."""
-    need = layout._dense_bytes
-    c = CacheDesc()
-    bufs = cache.bufs
-    k, v = bufs["k_dense"], bufs["v_dense"]
-    if not (k.device == device == v.device and k.nbytes >= need <= v.nbytes and k.is_contiguous()
-            and v.is_contiguous()):
-        raise ValueError(f"cache.k_dense and v_dense must be contiguous buffers of {need} bytes on {device}")
-    c.k_dense = k.data_ptr()
-    c.v_dense = v.data_ptr()
-    c.n_tokens = cache.n_tokens
-    c.layer = cache.layer
-    if cache.seq_lens is not None:
-        import torch
-
-        c.seq_lens = _tensor(cache.seq_lens, "cache.seq_lens", torch.int32, (batch,), device)
-    return c
-
-
-def _workspace(ws, device):
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous buffer on {device}")
-    return ws.data_ptr(), ws.nbytes
 
 
 def window_attn(layout: Layout, cache: Cache, q, out, ws, window, sinks=0, stream=None):
@@ -578,33 +550,18 @@ def window_attn(layout: Layout, cache: Cache, q, out, ws, window, sinks=0, strea
     seeing the last `window` tokens up to itself and the first `sinks`.
     q bf16 [B, Hq, n_q, d]; out fp32 or bf16 (the layout's) of the same shape;
     ws at least layout.window_workspace_bytes(cache.n_tokens, n_q) bytes."""
-    import torch
-
-    lead, B, Hq, _, d, _, out_type = _dense_dims(layout, cache)
-    dev = q.device
-    if q.dim() != 4 + len(lead):
-        raise ValueError("q must be [B, Hq, n_q, d] (all layers at once: [n_layers, B, Hq, n_q, d])")
-    n_q = q.shape[-2]
-    shape = (*lead, B, Hq, n_q, d)
-    qp = _tensor(q, "q", torch.bfloat16, shape, dev)
-    op = _tensor(out, "out", out_type, shape, dev)
-    c = _dense_cache(layout, cache, dev, B)
-    _run(dev, stream, lib().kvc_window_attn, layout.h, c, qp, n_q, window, sinks, op, *_workspace(ws, dev))
+    d, b = layout.dense(), cache.bufs
+    _checked(_ext.window_attn(d, b["k_dense"], b["v_dense"], cache.seq_lens, cache.n_tokens, cache.layer, q, out, ws,
+                              window, sinks, _stream(stream)))
 
 
 def decode_accum(layout: Layout, cache: Cache, q, weights, out, ws, stream=None):
     """kvc_decode_accum: single-token decode that adds every token's attention
     weight to weights fp32 [B, Hkv, max_tokens].  q bf16 [B, Hq, d]; out fp32 or
     bf16 of that shape; ws at least layout.accum_workspace_bytes(cache.n_tokens)."""
-    import torch
-
-    lead, B, Hq, Hkv, d, cap, out_type = _dense_dims(layout, cache)
-    dev, shape = q.device, (*lead, B, Hq, d)
-    qp = _tensor(q, "q", torch.bfloat16, shape, dev)
-    op = _tensor(out, "out", out_type, shape, dev)
-    ap = _tensor(weights, "weights", torch.float32, (*lead, B, Hkv, cap), dev)
-    c = _dense_cache(layout, cache, dev, B)
-    _run(dev, stream, lib().kvc_decode_accum, layout.h, c, qp, ap, op, *_workspace(ws, dev))
+    d, b = layout.dense(), cache.bufs
+    _checked(_ext.decode_accum(d, b["k_dense"], b["v_dense"], cache.seq_lens, cache.n_tokens, cache.layer, q, weights,
+                               out, ws, _stream(stream)))
 
 
 def evict(src_layout: Layout, src_cache: Cache, dst_layout: Layout, dst_cache: Cache, weights, dst_weights,
@@ -614,19 +571,11 @@ def evict(src_layout: Layout, src_cache: Cache, dst_layout: Layout, dst_cache: C
     dst_cache (which may be src_cache) and dst_weights.  Returns (kept int32
     [B, Hkv, keep], new_lens int32 [B]).  The caller sets the destination's
     n_tokens and seq_lens (new_lens) afterwards."""
-    import torch
-
-    lead, B, _, Hkv, _, cap, _ = _dense_dims(src_layout, src_cache)
-    lead2, B2, _, Hkv2, _, cap2, _ = _dense_dims(dst_layout, dst_cache)
-    dev = weights.device
-    ap = _tensor(weights, "weights", torch.float32, (*lead, B, Hkv, cap), dev)
-    bp = _tensor(dst_weights, "dst_weights", torch.float32, (*lead2, B2, Hkv2, cap2), dev)
-    a = _dense_cache(src_layout, src_cache, dev, B)
-    b = _dense_cache(dst_layout, dst_cache, dev, B2)
-    kept = weights.new_empty((*lead, B, Hkv, max(0, int(keep))), dtype=torch.int32)
-    lens = weights.new_empty((B,), dtype=torch.int32)
-    _run(dev, stream, lib().kvc_evict, src_layout.h, a, dst_layout.h, b, ap, bp, keep, sinks, recent,
-         kept.data_ptr() or None, lens.data_ptr())
+    a, b, s, t = src_layout.dense(), dst_layout.dense(), src_cache.bufs, dst_cache.bufs
+    status, kept, lens = _ext.evict(a, s["k_dense"], s["v_dense"], src_cache.seq_lens, src_cache.n_tokens,
+                                    src_cache.layer, b, t["k_dense"], t["v_dense"], dst_cache.layer, weights,
+                                    dst_weights, keep, sinks, recent, _stream(stream))
+    _checked(status)
     return kept, lens
 
 
@@ -636,13 +585,7 @@ def prefix_decode(prefix_layout: Layout, prefix_cache: Cache, layout: Layout, ca
     prefix_cache (a dense cache of batch 1) and continue with their own in cache.
     q bf16 [B, Hq, d]; out fp32 or bf16 of that shape; ws at least
     layout.prefix_workspace_bytes(cache.n_tokens, prefix_cache.n_tokens) bytes."""
-    import torch
-
-    lead, B, Hq, _, d, _, out_type = _dense_dims(layout, cache)
-    _dense_dims(prefix_layout, prefix_cache)
-    dev, shape = q.device, (*lead, B, Hq, d)
-    qp = _tensor(q, "q", torch.bfloat16, shape, dev)
-    op = _tensor(out, "out", out_type, shape, dev)
-    a = _dense_cache(prefix_layout, prefix_cache, dev, 1)
-    b = _dense_cache(layout, cache, dev, B)
-    _run(dev, stream, lib().kvc_prefix_decode, prefix_layout.h, a, layout.h, b, qp, op, *_workspace(ws, dev))
+    a, d, p, b = prefix_layout.dense(), layout.dense(), prefix_cache.bufs, cache.bufs
+    _checked(_ext.prefix_decode(a, p["k_dense"], p["v_dense"], prefix_cache.seq_lens, prefix_cache.n_tokens,
+                                prefix_cache.layer, d, b["k_dense"], b["v_dense"], cache.seq_lens, cache.n_tokens,
+                                cache.layer, q, out, ws, _stream(stream)))
